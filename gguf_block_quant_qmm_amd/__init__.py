@@ -29,6 +29,17 @@ there is no CPU fallback.
     qmm_gemv_q8act / qmm_gemv_concat_q8act / qmm_gemv_swiglu_q8act /
     qmm_gemv_argmax_q8act                            the decode calls above with x
                                                      quantized inside the launch
+    qmm_block_norm(residual, N, K, residual_out=None, block=None, w_post=None, gate=None,
+                   gate_stride=0, scale=1.0, w_pre=None, eps=1e-5, H=None, scales=None,
+                   quants=None, stream=None)         the norms after and before a block with
+                                                     its gate and residual scale
+    qmm_moe_route(logits, N, E, topk, ids, weights, bias=None, scoring=QMM_ROUTE_SOFTMAX,
+                  groups=1, topk_groups=1, group_top=1, renorm=True, scale=1.0, stream=None)
+                                                     each token's topk experts and weights
+    qmm_moe_swiglu(gate, up, dtype, E, M, K, N, T, ids, X, out, work=None, stream=None)
+                                                     out[n][t] = silu(G_e x_n) * (U_e x_n)
+    qmm_moe_down(w, dtype, E, M, K, N, T, ids, weights, H, Y, residual=None, work=None,
+                 stream=None)                        Y[n] = residual[n] + sum_t w_nt W_e h_nt
 """
 from __future__ import annotations
 
@@ -43,17 +54,20 @@ QMM_Q4_0, QMM_Q4_1, QMM_Q8_0, QMM_Q4_K, QMM_Q5_K, QMM_Q6_K = 2, 3, 8, 12, 13, 14
 DTYPES = {"Q4_0": QMM_Q4_0, "Q4_1": QMM_Q4_1, "Q8_0": QMM_Q8_0, "Q4_K": QMM_Q4_K, "Q5_K": QMM_Q5_K,
           "Q6_K": QMM_Q6_K}
 QMM_OK, QMM_ERR_NULL, QMM_ERR_DTYPE, QMM_ERR_SHAPE = 0, -1, -2, -3
-QMM_ERR_ALIGN, QMM_ERR_DEVICE, QMM_ERR_LAUNCH, QMM_ERR_SCRATCH = -4, -5, -6, -7
+QMM_ERR_ALIGN, QMM_ERR_DEVICE, QMM_ERR_LAUNCH, QMM_ERR_SCRATCH, QMM_ERR_VALUE = -4, -5, -6, -7, -8
 
 QMM_GEMV_MAX_MATS = 4
 QMM_ARGMAX_WORK_BYTES = 32768
 QMM_NOALLOC_SCRATCH_BYTES = 32768
 QMM_READ_PROBE_OUT_FLOATS = 4096
+QMM_ROUTE_SOFTMAX, QMM_ROUTE_SIGMOID = 0, 1
+QMM_MOE_MAX_EXPERTS, QMM_MOE_MAX_TOPK = 1024, 32
 
 EXPORTS = ("qmm_gemv", "qmm_gemv_concat", "qmm_gemv_swiglu", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_gemm", "qmm_gemm_swiglu",
            "qmm_quantize_q8_0", "qmm_gemm_q8act", "qmm_gemv_q8act", "qmm_gemv_concat_q8act",
            "qmm_gemv_swiglu_q8act", "qmm_gemv_argmax_q8act", "qmm_repack_bytes", "qmm_repack", "qmm_gemm_repacked", "qmm_gemm_repacked_kernel",
-           "qmm_gemm_path", "qmm_gemm_q8act_path", "qmm_gemm_kernel", "qmm_gemm_swiglu_kernel", "qmm_read_probe", "qmm_blob_bytes", "qmm_block_elems",
+           "qmm_block_norm", "qmm_moe_route", "qmm_moe_swiglu_work_bytes", "qmm_moe_swiglu", "qmm_moe_down_work_bytes",
+           "qmm_moe_down", "qmm_gemm_path", "qmm_gemm_q8act_path", "qmm_gemm_kernel", "qmm_gemm_swiglu_kernel", "qmm_read_probe", "qmm_blob_bytes", "qmm_block_elems",
            "qmm_block_bytes", "qmm_strerror")
 
 _lib = None
@@ -117,6 +131,18 @@ def lib():
         L.qmm_gemm_kernel.restype = ci
         L.qmm_read_probe.argtypes = [vp, i64, vp, vp]
         L.qmm_read_probe.restype = ci
+        f32 = ctypes.c_float
+        L.qmm_block_norm.argtypes = [vp, vp, vp, i64, f32, vp, vp, vp, f32, i64, i64, vp, vp, vp, vp]
+        L.qmm_block_norm.restype = ci
+        L.qmm_moe_route.argtypes = [vp, vp, i64, i64, ci, i64, i64, ci, i64, ci, f32, vp, vp, vp]
+        L.qmm_moe_route.restype = ci
+        for f in (L.qmm_moe_swiglu_work_bytes, L.qmm_moe_down_work_bytes):
+            f.argtypes = [ci, i64, i64, i64, i64, i64]
+            f.restype = i64
+        L.qmm_moe_swiglu.argtypes = [vp, vp, ci, i64, i64, i64, i64, i64, vp, vp, vp, vp, i64, vp]
+        L.qmm_moe_swiglu.restype = ci
+        L.qmm_moe_down.argtypes = [vp, ci, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp]
+        L.qmm_moe_down.restype = ci
         L.qmm_blob_bytes.argtypes = [ci, i64, i64]
         L.qmm_blob_bytes.restype = i64
         L.qmm_block_elems.argtypes = [ci]
@@ -368,3 +394,71 @@ def qmm_gemv_argmax_q8act(w, dtype: int, M: int, K: int, x, work, index, value=N
                                      _stream(stream))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_gemv_argmax_q8act")
+
+
+def qmm_block_norm(residual, N: int, K: int, residual_out=None, block=None, w_post=None, gate=None,
+                   gate_stride: int = 0, scale: float = 1.0, w_pre=None, eps: float = 1e-5, H=None, scales=None,
+                   quants=None, stream=None) -> None:
+    import torch
+    f32, row, nb = torch.float32, 4 * N * K, (K // 32 if K > 0 else 0)
+    rc = lib().qmm_block_norm(_addr(block, row, "block", f32), _addr(w_post, 4 * K, "w_post", f32),
+                              _addr(gate, row if gate_stride else 4 * K, "gate", f32), gate_stride, scale,
+                              _addr(residual, row, "residual", f32), _addr(residual_out, row, "residual_out", f32),
+                              _addr(w_pre, 4 * K, "w_pre", f32), eps, N, K, _addr(H, row, "H", f32),
+                              _addr(scales, 4 * N * nb, "scales", f32), _addr(quants, N * K, "quants", torch.int8),
+                              _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_block_norm")
+
+
+def qmm_moe_route(logits, N: int, E: int, topk: int, ids, weights, bias=None, scoring: int = QMM_ROUTE_SOFTMAX,
+                  groups: int = 1, topk_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+                  stream=None) -> None:
+    import torch
+    rc = lib().qmm_moe_route(_addr(logits, 4 * N * E, "logits", torch.float32), _addr(bias, 4 * E, "bias", torch.float32),
+                             N, E, scoring, groups, topk_groups, group_top, topk, int(bool(renorm)), scale,
+                             _addr(ids, 4 * N * topk, "ids", torch.int32),
+                             _addr(weights, 4 * N * topk, "weights", torch.float32), _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_moe_route")
+
+
+def moe_swiglu_work_bytes(dtype: int, E: int, M: int, K: int, N: int, T: int) -> int:
+    """Bytes of work that qmm_moe_swiglu needs for these sizes (0: none)."""
+    return lib().qmm_moe_swiglu_work_bytes(dtype, E, M, K, N, T)
+
+
+def moe_down_work_bytes(dtype: int, E: int, M: int, K: int, N: int, T: int) -> int:
+    """Bytes of work that qmm_moe_down needs for these sizes (0: none)."""
+    return lib().qmm_moe_down_work_bytes(dtype, E, M, K, N, T)
+
+
+def _work(work) -> tuple[int, int]:
+    """Address and bytes of a work tensor (None or an empty one: no work)."""
+    if work is None:
+        return 0, 0
+    return _addr(work, None, "work"), work.numel() * work.element_size()
+
+
+def qmm_moe_swiglu(gate, up, dtype: int, E: int, M: int, K: int, N: int, T: int, ids, X, out, work=None,
+                   stream=None) -> None:
+    import torch
+    nb = E * blob_bytes(dtype, M, K) or None
+    rc = lib().qmm_moe_swiglu(_addr(gate, nb, "gate"), _addr(up, nb, "up"), dtype, E, M, K, N, T,
+                              _addr(ids, 4 * N * T, "ids", torch.int32), _addr(X, 4 * N * K, "X", torch.float32),
+                              _addr(out, 4 * N * T * M, "out", torch.float32), *_work(work), _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_moe_swiglu")
+
+
+def qmm_moe_down(w, dtype: int, E: int, M: int, K: int, N: int, T: int, ids, weights, H, Y, residual=None, work=None,
+                 stream=None) -> None:
+    import torch
+    rc = lib().qmm_moe_down(_addr(w, E * blob_bytes(dtype, M, K) or None, "w_blob"), dtype, E, M, K, N, T,
+                            _addr(ids, 4 * N * T, "ids", torch.int32),
+                            _addr(weights, 4 * N * T, "weights", torch.float32),
+                            _addr(H, 4 * N * T * K, "H", torch.float32),
+                            _addr(residual, 4 * N * M, "residual", torch.float32),
+                            _addr(Y, 4 * N * M, "Y", torch.float32), *_work(work), _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_moe_down")

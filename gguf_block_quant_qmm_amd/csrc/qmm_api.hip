@@ -3,8 +3,10 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "qmm.h"
@@ -147,6 +149,24 @@ int64_t mfma_from_n(int dtype, int64_t M, int64_t K) {
     return (dtype == QMM_Q4_0 || dtype == QMM_Q6_K) ? 3 : 2;
 }
 
+// Sizes of the routed experts' products: every index of a slot fits int32 and
+// every byte offset 63 bits.
+int check_moe(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
+    const int rc = check_shape(dtype, M, K, N);
+    if (rc != QMM_OK) return rc;
+    if (E < 1 || E > QMM_MOE_MAX_EXPERTS || T < 1 || T > QMM_MOE_MAX_TOPK || N > INT32_MAX / T) return QMM_ERR_SHAPE;
+    constexpr int64_t kMaxProd = int64_t(1) << 56;
+    if (M * K > kMaxProd / E || M > kMaxProd / (N * T) || K > kMaxProd / (N * T)) return QMM_ERR_SHAPE;
+    return QMM_OK;
+}
+
+int check_work(const void *work, int64_t work_bytes, int64_t need) {
+    if (need == 0) return QMM_OK;
+    if (!work) return QMM_ERR_NULL;
+    if (!aligned(work, 16)) return QMM_ERR_ALIGN;
+    return work_bytes < need ? QMM_ERR_SCRATCH : QMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -168,7 +188,8 @@ const char *qmm_strerror(int code) {
     case QMM_ERR_ALIGN: return "misaligned pointer (blob and x/X need 16-byte, y/Y 4-byte alignment)";
     case QMM_ERR_DEVICE: return "no current HIP device, or it is not gfx950";
     case QMM_ERR_LAUNCH: return "kernel launch failed";
-    case QMM_ERR_SCRATCH: return "the call needs more scratch than the library's static buffer holds";
+    case QMM_ERR_SCRATCH: return "the call needs more scratch than work_bytes, or than the library's static buffer holds";
+    case QMM_ERR_VALUE: return "a scalar argument is out of range (scoring, or a scale or eps that is not finite)";
     default: return "unknown status code";
     }
 }
@@ -477,6 +498,90 @@ int qmm_gemm(const void *w_blob, int dtype, int64_t M, int64_t K, int64_t N, con
     } else {
         e = qmm::launch_gemm_mfma(dtype, w_blob, M, K, N, X, Y, (hipStream_t)stream);
     }
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int qmm_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride, float scale,
+                   const float *residual, float *residual_out, const float *w_pre, float eps, int64_t N, int64_t K,
+                   float *H, float *scales, int8_t *quants, void *stream) {
+    if (N < 1 || N > INT32_MAX || K < 1 || K > (int64_t(1) << 28)) return QMM_ERR_SHAPE;
+    if (block && gate && gate_stride != 0 && gate_stride != K) return QMM_ERR_SHAPE;
+    if (quants && K % 32 != 0) return QMM_ERR_SHAPE;
+    if (!std::isfinite(scale) || !std::isfinite(eps) || eps < 0.f) return QMM_ERR_VALUE;
+    if (!residual || (block && !residual_out) || (!scales != !quants)) return QMM_ERR_NULL;
+    if (!residual_out && !H && !quants) return QMM_ERR_NULL;  // nothing to write
+    for (const void *p : {(const void *)block, (const void *)w_post, (const void *)gate, (const void *)residual,
+                          (const void *)residual_out, (const void *)w_pre, (const void *)H, (const void *)scales,
+                          (const void *)quants})
+        if (!aligned(p, 16)) return QMM_ERR_ALIGN;
+    int cus = 0;
+    const int rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e = qmm::launch_block_norm(block, w_post, gate, gate_stride, scale, residual, residual_out, w_pre,
+                                                eps, N, K, H, scales, quants, (hipStream_t)stream);
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, int scoring, int64_t groups,
+                  int64_t topk_groups, int group_top, int64_t topk, int renorm, float scale, int32_t *ids,
+                  float *weights, void *stream) {
+    if (N < 1 || N > INT32_MAX || E < 1 || E > QMM_MOE_MAX_EXPERTS) return QMM_ERR_SHAPE;
+    if (groups < 1 || groups > E || E % groups != 0 || topk_groups < 1 || topk_groups > groups) return QMM_ERR_SHAPE;
+    if (group_top < 1 || group_top > 2 || group_top > E / groups) return QMM_ERR_SHAPE;
+    if (topk < 1 || topk > QMM_MOE_MAX_TOPK || topk > topk_groups * (E / groups)) return QMM_ERR_SHAPE;
+    if ((scoring != QMM_ROUTE_SOFTMAX && scoring != QMM_ROUTE_SIGMOID) || !std::isfinite(scale)) return QMM_ERR_VALUE;
+    if (!logits || !ids || !weights) return QMM_ERR_NULL;
+    if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return QMM_ERR_ALIGN;
+    int cus = 0;
+    const int rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e =
+        qmm::launch_moe_route(logits, bias, N, E, scoring == QMM_ROUTE_SIGMOID, groups, topk_groups, group_top, topk,
+                              renorm != 0, scale, ids, weights, (hipStream_t)stream);
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int64_t qmm_moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
+    return check_moe(dtype, E, M, K, N, T) == QMM_OK ? qmm::moe_swiglu_work_bytes(dtype, E, M, K, N, T) : 0;
+}
+
+int64_t qmm_moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
+    return check_moe(dtype, E, M, K, N, T) == QMM_OK ? qmm::moe_down_work_bytes(dtype, E, M, K, N, T) : 0;
+}
+
+int qmm_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T,
+                   const int32_t *ids, const float *X, float *out, void *work, int64_t work_bytes, void *stream) {
+    int rc = check_moe(dtype, E, M, K, N, T);
+    if (rc != QMM_OK) return rc;
+    if (!gate || !up || !ids || !X || !out) return QMM_ERR_NULL;
+    if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(ids, 4) || !aligned(X, 16) || !aligned(out, 4))
+        return QMM_ERR_ALIGN;
+    rc = check_work(work, work_bytes, qmm::moe_swiglu_work_bytes(dtype, E, M, K, N, T));
+    if (rc != QMM_OK) return rc;
+    int cus = 0;
+    rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e =
+        qmm::launch_moe_swiglu(gate, up, dtype, E, M, K, N, T, ids, X, out, work, (hipStream_t)stream, cus);
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int qmm_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, const int32_t *ids,
+                 const float *weights, const float *H, const float *residual, float *Y, void *work, int64_t work_bytes,
+                 void *stream) {
+    int rc = check_moe(dtype, E, M, K, N, T);
+    if (rc != QMM_OK) return rc;
+    if (!w || !ids || !weights || !H || !Y) return QMM_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(H, 16) || !aligned(residual, 4) ||
+        !aligned(Y, 4))
+        return QMM_ERR_ALIGN;
+    rc = check_work(work, work_bytes, qmm::moe_down_work_bytes(dtype, E, M, K, N, T));
+    if (rc != QMM_OK) return rc;
+    int cus = 0;
+    rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e = qmm::launch_moe_down(w, dtype, E, M, K, N, T, ids, weights, H, residual, Y, work,
+                                              (hipStream_t)stream, cus);
     return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 

@@ -106,4 +106,27 @@ hipError_t launch_gemm_q8act_mfma(int dtype, const void *blob, int64_t M, int64_
 hipError_t launch_gemv_q8in(int mode, int n, const void *const *blobs, const int64_t *Ms, int dtype, int64_t K,
                             const float *x, float *const *ys, hipStream_t st, int cus);
 
+// The norms after and before a block with its gate and residual scale
+// (qmm_norm.hip): K <= 2^28, block / w_post / gate / residual_out / w_pre / H /
+// (scales, quants) may be NULL as qmm_block_norm allows.
+hipError_t launch_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride,
+                             float scale, const float *residual, float *residual_out, const float *w_pre, float eps,
+                             int64_t N, int64_t K, float *H, float *scales, int8_t *quants, hipStream_t st);
+
+// Routing (qmm_route.hip): E <= QMM_MOE_MAX_EXPERTS, topk <= QMM_MOE_MAX_TOPK.
+hipError_t launch_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, bool sigmoid, int64_t groups,
+                            int64_t topk_groups, int group_top, int64_t topk, bool renorm, float scale, int32_t *ids,
+                            float *weights, hipStream_t st);
+
+// The routed experts' products (qmm_moe.hip).  `work` holds the work bytes of
+// the same sizes (NULL where they are 0).
+int64_t moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
+int64_t moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
+hipError_t launch_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N,
+                             int64_t T, const int32_t *ids, const float *X, float *out, void *work, hipStream_t st,
+                             int cus);
+hipError_t launch_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T,
+                           const int32_t *ids, const float *weights, const float *H, const float *residual, float *Y,
+                           void *work, hipStream_t st, int cus);
+
 }  // namespace qmm

@@ -82,7 +82,10 @@ extern "C" {
 #define QMM_ERR_ALIGN (-4)   /* blob not 16-B aligned, x/X not 16-B, y/Y not 4-B    */
 #define QMM_ERR_DEVICE (-5)  /* no current HIP device, or it is not gfx950          */
 #define QMM_ERR_LAUNCH (-6)  /* the kernel launch itself failed                     */
-#define QMM_ERR_SCRATCH (-7) /* needs more than the static scratch (no-alloc calls) */
+#define QMM_ERR_SCRATCH (-7) /* needs more than the static scratch (no-alloc calls)
+                                or than the work_bytes it was given             */
+#define QMM_ERR_VALUE (-8)   /* a scalar argument has no meaning (an unknown
+                                scoring, a scale or eps that is not finite, ...)  */
 
 /* Decode GEMV (one token), page "cera 0.5.2 src/backend/cpu.rs", section
  * "GEMV (matrix-vector multiply)": y[m] = sum_k W[m][k] * x[k].
@@ -329,6 +332,104 @@ int qmm_repack(const void *w_blob, int dtype, int64_t M, int64_t K, void *packed
 int qmm_gemm_repacked(const void *packed, int dtype, int64_t M, int64_t K, int64_t N, const float *X,
                       float *Y, void *stream);
 int qmm_gemm_repacked_kernel(int dtype, int64_t M, int64_t K, int64_t N);
+
+/* The norms after and before a block, fused with the block's gate and residual
+ * scale (page "cera 0.5.2 src/backend/cpu.rs": rmsnorm and the fused
+ * rmsnorm + Q8_0 quantization; page "cera 0.3.1 src/model/gpu_lfm2.rs": the
+ * batched add + rmsnorm pipeline).  Per token n, over its K values:
+ *     p = block[n], or, with w_post, block[n] / sqrt(mean(block[n]^2) + eps) * w_post
+ *     r = residual[n] + scale * gate * p        -> residual_out[n]
+ *     h = r / sqrt(mean(r^2) + eps) * w_pre     -> H[n], and/or its Q8_0 blocks
+ * Computed in f64; r and h are rounded to f32 once, and h is computed from the
+ * rounded r.  The Q8_0 blocks are those qmm_quantize_q8_0 makes of the f32 h
+ * (the bits it writes), ready for qmm_gemm_q8act.
+ *   block        device f32 [N][K], or NULL: r = residual (a plain norm)
+ *   w_post       device f32 [K], or NULL: no norm after the block
+ *   gate         device f32, or NULL: 1.  gate_stride 0: [K], the same for
+ *                every token; gate_stride K: [N][K]
+ *   scale        the residual scale (finite)
+ *   residual     device f32 [N][K]
+ *   residual_out device f32 [N][K]; overwritten; may be `residual` itself;
+ *                may be NULL when block is NULL
+ *   w_pre        device f32 [K], or NULL: 1
+ *   eps          finite, >= 0 (0 and a zero row give NaN, as the formula does)
+ *   H            device f32 [N][K] or NULL
+ *   scales, quants  device f32 [N][K/32] and int8 [N][K] as qmm_quantize_q8_0
+ *                writes them, or both NULL; need K a multiple of 32
+ * With neither H nor quants only residual_out is written.  block, w_post and
+ * gate without a block are ignored.  Apart from residual_out == residual the
+ * outputs overlap nothing.  1 <= N <= 2^31 - 1, 1 <= K <= 2^28; every pointer
+ * 16-B aligned. */
+int qmm_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride, float scale,
+                   const float *residual, float *residual_out, const float *w_pre, float eps, int64_t N, int64_t K,
+                   float *H, float *scales, int8_t *quants, void *stream);
+
+/* Routing of N tokens to topk of E experts each.  Per token, in f64:
+ *     s = softmax(logits) or 1 / (1 + e^-logits),  c = s + bias
+ *   The E experts form `groups` groups of E / groups neighbours.  A group's
+ *   score is the sum of its group_top (1 or 2) largest c; the topk_groups
+ *   groups with the largest scores stay open (equal scores: the lower group).
+ *   ids = the topk experts of open groups with the largest c, falling; equal c:
+ *   the lower index.  weights = s[ids], divided by their sum if renorm (all 0
+ *   if the sum is 0), times scale; rounded to f32 once.
+ * A logit of -inf or NaN masks its expert: score 0, and behind every expert
+ * with a larger c.  A row of nothing but those has scores 0.  A logit of +inf
+ * counts as the largest finite f32.  A NaN in c counts as -inf.
+ *   logits   device f32 [N][E], 4-B aligned
+ *   bias     device f32 [E] (a balance bias: it moves the choice, not the
+ *            weights), 4-B aligned, or NULL
+ *   scoring  QMM_ROUTE_SOFTMAX or QMM_ROUTE_SIGMOID, else QMM_ERR_VALUE
+ *   groups   divides E; 1 for no groups.  1 <= topk_groups <= groups,
+ *            group_top <= E / groups, topk <= topk_groups * (E / groups) and
+ *            QMM_MOE_MAX_TOPK, 1 <= E <= QMM_MOE_MAX_EXPERTS, 1 <= N <= 2^31 - 1:
+ *            else QMM_ERR_SHAPE
+ *   scale    finite, else QMM_ERR_VALUE
+ *   ids      device int32 [N][topk], weights device f32 [N][topk], 4-B aligned;
+ *            overwritten */
+#define QMM_ROUTE_SOFTMAX 0
+#define QMM_ROUTE_SIGMOID 1
+#define QMM_MOE_MAX_EXPERTS 1024
+#define QMM_MOE_MAX_TOPK 32
+int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, int scoring, int64_t groups,
+                  int64_t topk_groups, int group_top, int64_t topk, int renorm, float scale, int32_t *ids,
+                  float *weights, void *stream);
+
+/* The routed experts' gate/up projections with SwiGLU.  Token n has T slots;
+ * slot (n, t) goes through expert e = ids[n][t]:
+ *     out[n][t][m] = silu(G_e x_n)[m] * (U_e x_n)[m]      (silu as qmm_gemv_swiglu)
+ * An id outside 0 .. E-1 (padding: -1) is no expert: out[n][t] is all zeros.
+ * An expert may stand in several slots of a token.
+ *   gate, up  device blobs of E matrices of M x K weights of one dtype, matrix
+ *             e at byte e * qmm_blob_bytes(dtype, M, K) (the GGUF layout of a
+ *             three-dimensional expert tensor), 16-B aligned
+ *   ids       device int32 [N][T], 4-B aligned
+ *   X         device f32 [N][K], 16-B aligned
+ *   out       device f32 [N][T][M], 4-B aligned; overwritten
+ *   work      device scratch of at least qmm_moe_swiglu_work_bytes(...) bytes
+ *             (work_bytes; less is QMM_ERR_SCRATCH), 16-B aligned; NULL where
+ *             that is 0.  Needs no initial value; clobbered.  Calls that overlap
+ *             in time (two streams, two captured graphs) need separate work.
+ * Both projections are f32 class for every N: with S the sum of |w x|
+ * of a projection, |error| <= 1e-5 * S.  1 <= E <= QMM_MOE_MAX_EXPERTS,
+ * 1 <= T <= QMM_MOE_MAX_TOPK, N * T <= 2^31 - 1, any K the dtype allows. */
+int64_t qmm_moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
+int qmm_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T,
+                   const int32_t *ids, const float *X, float *out, void *work, int64_t work_bytes, void *stream);
+
+/* The routed experts' down projection, their weighted sum and the residual:
+ *     Y[n][m] = residual[n][m] + sum_t weights[n][t] * (W_e h_nt)[m],  e = ids[n][t]
+ * A slot whose id is outside 0 .. E-1 adds nothing, whatever its weight and h.
+ *   w         device blob of E matrices of M x K weights, as gate above
+ *   weights   device f32 [N][T], 4-B aligned
+ *   H         device f32 [N][T][K], 16-B aligned (what qmm_moe_swiglu writes)
+ *   residual  device f32 [N][M], 4-B aligned, or NULL: 0.  May be Y itself.
+ *   Y         device f32 [N][M], 4-B aligned; overwritten
+ *   ids, work, work_bytes and sizes as above, with qmm_moe_down_work_bytes
+ * The slots are summed in a fixed order. */
+int64_t qmm_moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
+int qmm_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, const int32_t *ids,
+                 const float *weights, const float *H, const float *residual, float *Y, void *work, int64_t work_bytes,
+                 void *stream);
 
 /* Which arithmetic qmm_gemm uses for these sizes: 0 = f32 (GEMV family),
  * 1 = f16 matrix-core GEMM, or a negative status for invalid arguments. */

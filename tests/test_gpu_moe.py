@@ -1,0 +1,282 @@
+"""qmm_moe_swiglu and qmm_moe_down on the GPU against the f64 oracle.
+
+Tolerances, from the documented bounds.  With S the sum of |w x| of a
+projection the f32-class products are within tau = 1e-5 of S.  SwiGLU:
+    |out - exact| <= tau (1.1 S_g (|u| + tau S_u) + |silu(g)| S_u) + 4 2^-24 |out|
+(|silu'| < 1.1; silu and the product add four f32 roundings).  Down: each
+slot's product within tau S, one rounding per multiply-add of the T slots and
+the residual: sum_t |w_t| tau S_t + (T + 1) 2^-24 (sum_t |w_t y_t| + |res|).
+"""
+import numpy as np
+import pytest
+import torch
+
+import gguf_block_quant_qmm_amd as q
+import oracle
+from qmm_inputs import GEOMETRY, NAMES, make_blob, make_x, rng_for
+
+pytestmark = pytest.mark.gpu
+
+TAU = 1e-5
+DTYPES = sorted(NAMES)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+
+
+def dev(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def experts(dt, E, M, K, seed):
+    return np.concatenate([make_blob(dt, M, K, rng_for(2100 + seed, e)) for e in range(E)])
+
+
+def slot_products(dt, blob, E, M, K, ids, rows):
+    """(Y64, bound sums) of every slot's product; zeros where the id is no expert."""
+    nb = M * (K // GEOMETRY[dt][0]) * GEOMETRY[dt][1]
+    y, S = np.zeros((len(ids), M)), np.zeros((len(ids), M))
+    for e in range(E):
+        at = np.nonzero(ids == e)[0]
+        if at.size:
+            _, y[at], S[at] = oracle.matmul(dt, blob[e * nb:(e + 1) * nb], M, K, np.ascontiguousarray(rows[at]))
+    return y, S
+
+
+def silu(v):
+    return v * np.where(v >= 0, 1.0 / (1.0 + np.exp(-np.abs(v))), np.exp(-np.abs(v)) / (1.0 + np.exp(-np.abs(v))))
+
+
+def work_of(n, fill=0xA5):
+    return torch.full((n,), fill, dtype=torch.uint8, device="cuda") if n else None
+
+
+def run_swiglu(dt, E, M, K, N, T, ids, gate, up, X, stream=None):
+    out = torch.full((N * T + 1, M), 7.0, device="cuda")
+    q.qmm_moe_swiglu(gate, up, dt, E, M, K, N, T, ids, X, out[:N * T], work=work_of(q.moe_swiglu_work_bytes(dt, E, M, K, N, T)),
+                     stream=stream)
+    torch.cuda.synchronize()
+    assert torch.all(out[N * T] == 7.0)
+    return out[:N * T]
+
+
+def check_swiglu(dt, E, M, K, N, T, ids=None, seed=0, X=None, S_of=None):
+    g = np.random.default_rng([21, dt, E, M, K, N, T, seed])
+    ids = g.integers(0, E, (N, T), dtype=np.int32) if ids is None else np.asarray(ids, np.int32).reshape(N, T)
+    G, U = experts(dt, E, M, K, seed), experts(dt, E, M, K, seed + 1)
+    X = make_x(N, K, g) if X is None else X
+    out = run_swiglu(dt, E, M, K, N, T, dev(ids), dev(G), dev(U), dev(X)).cpu().numpy().astype(np.float64)
+    rows = np.repeat(X, T, axis=0)
+    gv, Sg = slot_products(dt, G, E, M, K, ids.reshape(-1), rows)
+    uv, Su = slot_products(dt, U, E, M, K, ids.reshape(-1), rows)
+    want = silu(gv) * uv
+    tol = TAU * (1.1 * Sg * (np.abs(uv) + TAU * Su) + np.abs(silu(gv)) * Su) + 4 * 2.0 ** -24 * np.abs(want)
+    bad = np.abs(out - want) > tol
+    assert not bad.any(), f"{bad.sum()} of {bad.size}, worst {np.max(np.abs(out - want) / np.maximum(tol, 1e-300)):.3g} of the bound"
+    none = (ids.reshape(-1) < 0) | (ids.reshape(-1) >= E)
+    assert np.all(out[none] == 0.0)
+
+
+def check_down(dt, E, M, K, N, T, ids=None, seed=0, residual=True, in_place=False, H=None):
+    g = np.random.default_rng([22, dt, E, M, K, N, T, seed])
+    ids = g.integers(0, E, (N, T), dtype=np.int32) if ids is None else np.asarray(ids, np.int32).reshape(N, T)
+    W = experts(dt, E, M, K, seed)
+    H = make_x(N * T, K, g) if H is None else H
+    wt = g.standard_normal((N, T)).astype(np.float32)
+    none = (ids < 0) | (ids >= E)
+    wt[none] = np.nan                              # a skipped slot's weight and row are not looked at
+    H = H.copy()
+    H[none.reshape(-1)] = np.nan
+    R = g.standard_normal((N, M)).astype(np.float32) if residual else None
+    Y = torch.full((N + 1, M), 7.0, device="cuda")
+    Rd = dev(R)
+    if in_place:
+        Y[:N] = Rd
+        Rd = Y[:N]
+    q.qmm_moe_down(dev(W), dt, E, M, K, N, T, dev(ids), dev(wt), dev(H), Y[:N], residual=Rd,
+                   work=work_of(q.moe_down_work_bytes(dt, E, M, K, N, T)))
+    torch.cuda.synchronize()
+    assert torch.all(Y[N] == 7.0)
+    y, S = slot_products(dt, W, E, M, K, ids.reshape(-1), np.nan_to_num(H))
+    w = np.where(none, 0.0, np.nan_to_num(wt)).astype(np.float64)[:, :, None]
+    y, S = y.reshape(N, T, M), S.reshape(N, T, M)
+    res = R.astype(np.float64) if residual else 0.0
+    want = (w * y).sum(1) + res
+    tol = (np.abs(w) * TAU * S).sum(1) + (T + 1) * 2.0 ** -24 * (np.abs(w * y).sum(1) + np.abs(res))
+    err = np.abs(Y[:N].cpu().numpy().astype(np.float64) - want)
+    assert np.all(err <= tol), f"worst {np.max(err / np.maximum(tol, 1e-300)):.3g} of the bound"
+
+
+# block counts per row: one, odd, even; more units than a wavefront has lanes
+KS = {32: [32, 64, 96, 160, 1024, 2080, 4096, 4160], 256: [256, 512, 768, 1280, 4096, 4352]}
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+@pytest.mark.parametrize("M", [1, 3, 64, 130])
+def test_one_token(dt, M):
+    for K in KS[GEOMETRY[dt][0]]:
+        check_swiglu(dt, 4, M, K, 1, 2)
+        check_down(dt, 4, M, K, 1, 2)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+@pytest.mark.parametrize("N,T,E", [(2, 1, 1), (5, 3, 7), (7, 8, 16), (33, 4, 5), (150, 2, 3), (260, 1, 2)])
+def test_batches(dt, N, T, E):
+    bs = GEOMETRY[dt][0]
+    for K in (bs, 3 * bs, 2 * bs, 512):
+        for M in (5, 96):
+            check_swiglu(dt, E, M, K, N, T)
+            check_down(dt, E, M, K, N, T, residual=M == 96)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+def test_long_rows(dt):
+    for K in (8448, 14336, 16640):
+        check_swiglu(dt, 2, 9, K, 1, 2)
+        check_down(dt, 2, 9, K, 1, 2)
+        check_down(dt, 2, 33, K, 40, 2)
+        check_swiglu(dt, 2, 33, K, 40, 2)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 9, 31, 32])
+def test_slots_per_token(T):
+    for N in (1, 2, 40):
+        check_swiglu(q.QMM_Q4_0, 6, 70, 256, N, T)
+        check_down(q.QMM_Q6_K, 6, 70, 512, N, T)
+
+
+@pytest.mark.parametrize("N", [1, 6, 80])
+@pytest.mark.parametrize("dt", [q.QMM_Q4_0, q.QMM_Q6_K, q.QMM_Q5_K], ids=lambda d: NAMES[d])
+def test_padding_and_uneven_experts(dt, N):
+    E, M, K, T = 9, 75, 512, 3
+    g = np.random.default_rng(N)
+    ids = g.integers(0, E, (N, T), dtype=np.int32)
+    ids[0] = -1                                    # a token with no expert at all
+    ids[N // 2, 0] = E                             # just outside
+    ids[N - 1, T - 1] = np.int32(2 ** 31 - 1)
+    ids[N // 3, 1] = np.int32(-2 ** 31)
+    for I in (ids, np.full((N, T), -1), np.full((N, T), E - 1), np.zeros((N, T))):  # last: one expert, thrice per token
+        check_swiglu(dt, E, M, K, N, T, ids=I)
+        check_down(dt, E, M, K, N, T, ids=I)
+        check_down(dt, E, M, K, N, T, ids=I, in_place=True)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+@pytest.mark.parametrize("N", [1, 48])
+def test_scales_of_activations(dt, N):
+    """Rows of very different magnitudes beside each other, and within a row."""
+    E, M, K, T = 3, 40, 512, 2
+    g = np.random.default_rng(5)
+    X = make_x(N * T, K, g)
+    X *= (10.0 ** g.uniform(-12, 12, (N * T, 1))).astype(np.float32)
+    X[:, ::7] *= 1e-3
+    X[0, :] = 0.0
+    X[N * T - 1] *= 0.0 if N == 1 else 1.0
+    check_down(dt, E, M, K, N, T, H=X)
+    check_swiglu(dt, E, M, K, N, T, X=np.ascontiguousarray(X[:N]) if N > 1 else 1e-4 * make_x(1, K, g))
+
+
+def test_non_finite_rows_stay_in_their_token():
+    dt, E, M, K, T = q.QMM_Q4_K, 3, 64, 512, 2
+    for N in (4, 64):
+        g = np.random.default_rng(6)
+        ids = g.integers(0, E, (N, T), dtype=np.int32)
+        G, U, X = experts(dt, E, M, K, 0), experts(dt, E, M, K, 1), make_x(N, K, g)
+        clean = run_swiglu(dt, E, M, K, N, T, dev(ids), dev(G), dev(U), dev(X)).clone()
+        X[1, 5], X[2, 9] = np.nan, np.inf
+        got = run_swiglu(dt, E, M, K, N, T, dev(ids), dev(G), dev(U), dev(X))
+        same = [s for s in range(N * T) if s // T not in (1, 2)]
+        assert torch.equal(got[same], clean[same])
+        assert torch.all(torch.isnan(got[T:2 * T]))
+        assert not torch.any(torch.isfinite(got[2 * T:3 * T]) & (got[2 * T:3 * T] != 0))
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+def test_results_repeat_and_do_not_hang_on_neighbours(dt):
+    """Bitwise: run to run, and for a token moved elsewhere among the same tokens."""
+    E, M, K, T, N = 5, 96, 1024, 3, 70
+    g = np.random.default_rng(8)
+    ids, X = g.integers(0, E, (N, T), dtype=np.int32), make_x(N, K, g)
+    G, U = dev(experts(dt, E, M, K, 0)), dev(experts(dt, E, M, K, 1))
+    a = run_swiglu(dt, E, M, K, N, T, dev(ids), G, U, dev(X)).clone()
+    b = run_swiglu(dt, E, M, K, N, T, dev(ids), G, U, dev(X)).clone()
+    p = g.permutation(N)
+    c = run_swiglu(dt, E, M, K, N, T, dev(ids[p]), G, U, dev(X[p]))
+    assert torch.equal(a, b)
+    assert torch.equal(a.view(N, T, M)[torch.from_numpy(p).cuda()], c.view(N, T, M))
+
+
+@pytest.mark.parametrize("N", [1, 9, 96])
+def test_block_together(N):
+    """norm -> router product -> routing -> experts -> sum with the residual ->
+    next norm as Q8_0 -> the int8 product, eager on a side stream, then
+    captured and replayed on new inputs against eager runs."""
+    dt, E, T, K, M = q.QMM_Q4_K, 16, 4, 1024, 512
+    g = np.random.default_rng(N)
+    Wr = dev(make_blob(q.QMM_Q8_0, E, K, rng_for(2200, 0)))
+    G, U = dev(experts(dt, E, M, K, 0)), dev(experts(dt, E, M, K, 1))
+    D = dev(experts(q.QMM_Q6_K, E, K, M, 2))
+    Wq = dev(make_blob(q.QMM_Q8_0, 64, K, rng_for(2200, 1)))
+    w1, w2 = (dev((1 + 0.1 * g.standard_normal(K)).astype(np.float32)) for _ in range(2))
+    attn, x0 = dev(make_x(N, K, g)), dev(make_x(N, K, g))
+    e = lambda *s, dtype=torch.float32: torch.empty(s, device="cuda", dtype=dtype)
+    x1, h, lg, ids, wt = e(N, K), e(N, K), e(N, E), e(N, T, dtype=torch.int32), e(N, T)
+    act, x2, sc, qq, y = e(N, T, M), e(N, K), e(N, K // 32), e(N, K, dtype=torch.int8), e(N, 64)
+    ws = work_of(q.moe_swiglu_work_bytes(dt, E, M, K, N, T))
+    wd = work_of(q.moe_down_work_bytes(q.QMM_Q6_K, E, K, M, N, T))
+    outs = (x1, h, lg, ids, wt, act, x2, sc, qq, y)
+
+    def block():
+        q.qmm_block_norm(x0, N, K, residual_out=x1, block=attn, w_pre=w1, H=h)
+        q.qmm_gemm(Wr, q.QMM_Q8_0, E, K, N, h, lg)
+        q.qmm_moe_route(lg, N, E, T, ids, wt)
+        q.qmm_moe_swiglu(G, U, dt, E, M, K, N, T, ids, h, act, work=ws)
+        q.qmm_moe_down(D, q.QMM_Q6_K, E, K, M, N, T, ids, wt, act, x2, residual=x1, work=wd)
+        q.qmm_block_norm(x2, N, K, w_pre=w2, scales=sc, quants=qq)
+        q.qmm_gemm_q8act(Wq, q.QMM_Q8_0, 64, K, N, sc, qq, y)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block()
+    torch.cuda.synchronize()
+    # every step against f64 on the step's own inputs
+    n64 = lambda t: t.cpu().numpy().astype(np.float64)
+    assert np.allclose(n64(x1), n64(x0) + n64(attn), rtol=2.0 ** -23, atol=1e-12)
+    want = n64(x1) / np.sqrt((n64(x1) ** 2).mean(1, keepdims=True) + 1e-5) * n64(w1)
+    assert np.allclose(n64(h), want, rtol=2.0 ** -23, atol=0)
+    order = np.argsort(-n64(lg), axis=1, kind="stable")[:, :T]
+    assert np.array_equal(ids.cpu().numpy(), order)
+    s = np.exp(np.take_along_axis(n64(lg), order, 1))
+    # subnormal weights: the f32 step is 2^-149 whatever the value, half of it the rounding
+    assert np.allclose(n64(wt), s / s.sum(1, keepdims=True), rtol=2.0 ** -23, atol=2.0 ** -149)
+    idf, rows = ids.cpu().numpy().reshape(-1), np.repeat(h.cpu().numpy(), T, 0)
+    gv, Sg = slot_products(dt, G.cpu().numpy(), E, M, K, idf, rows)
+    uv, Su = slot_products(dt, U.cpu().numpy(), E, M, K, idf, rows)
+    tol = TAU * (1.1 * Sg * (np.abs(uv) + TAU * Su) + np.abs(silu(gv)) * Su) + 4 * 2.0 ** -24 * np.abs(silu(gv) * uv)
+    assert np.all(np.abs(n64(act).reshape(N * T, M) - silu(gv) * uv) <= tol)
+    yv, S = slot_products(q.QMM_Q6_K, D.cpu().numpy(), E, K, M, idf, act.cpu().numpy().reshape(N * T, M))
+    w = n64(wt)[:, :, None]
+    want, tol = (w * yv.reshape(N, T, K)).sum(1) + n64(x1), (w * TAU * S.reshape(N, T, K)).sum(1)
+    tol += (T + 1) * 2.0 ** -24 * ((w * np.abs(yv.reshape(N, T, K))).sum(1) + np.abs(n64(x1)))
+    assert np.all(np.abs(n64(x2) - want) <= tol)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block()
+    for i in range(4):
+        attn.normal_(), x0.normal_()
+        for t in outs:
+            t.zero_()
+        for t in (ws, wd):
+            if t is not None:
+                t.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        block()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, outs)), f"replay {i}"
