@@ -62,22 +62,25 @@ unsigned rows_grid(int64_t rows) {
 
 }  // namespace
 
-#define QMM_MOE_DT(dtype, CALL)                            \
-    switch (dtype) {                                       \
-    case QMM_Q4_0: CALL(QMM_Q4_0); break;                  \
-    case QMM_Q4_1: CALL(QMM_Q4_1); break;                  \
-    case QMM_Q8_0: CALL(QMM_Q8_0); break;                  \
-    case QMM_Q4_K: CALL(QMM_Q4_K); break;                  \
-    case QMM_Q5_K: CALL(QMM_Q5_K); break;                  \
-    case QMM_Q6_K: CALL(QMM_Q6_K); break;                  \
-    default: return hipErrorInvalidValue;                  \
-    }
+// Few tokens: a wavefront per row.  A tuning lever of measurement builds only.
+static bool use_gemm(int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
+    static const int lever = tuning_lever("QMM_MOE_GEMM_FROM_N", 8);
+    (void)E;
+    (void)T;
+    return moe_gemm_ok(M, K) && N >= lever;
+}
 
-int64_t moe_swiglu_work_bytes(int, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
-int64_t moe_down_work_bytes(int, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+int64_t moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
+    return use_gemm(E, M, K, N, T) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, false) : 0;
+}
+int64_t moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
+    return use_gemm(E, M, K, N, T) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, true) : 0;
+}
 
 hipError_t launch_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N,
-                             int64_t T, const int32_t *ids, const float *X, float *out, void *, hipStream_t st, int) {
+                             int64_t T, const int32_t *ids, const float *X, float *out, void *work, hipStream_t st,
+                             int) {
+    if (use_gemm(E, M, K, N, T)) return launch_moe_gemm_swiglu(gate, up, dtype, E, M, K, N, T, ids, X, out, work, st);
 #define QMM_CALL(DT)                                                                                                   \
     hipLaunchKernelGGL((moe_swiglu_rows_kernel<DT>), dim3(rows_grid(N *T *M)), dim3(256), 0, st, (const uint8_t *)gate, \
                        (const uint8_t *)up, (int)E, M, K, N *T, (int)T, ids, X, out)
@@ -88,7 +91,9 @@ hipError_t launch_moe_swiglu(const void *gate, const void *up, int dtype, int64_
 
 hipError_t launch_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T,
                            const int32_t *ids, const float *weights, const float *H, const float *residual, float *Y,
-                           void *, hipStream_t st, int) {
+                           void *work, hipStream_t st, int) {
+    if (use_gemm(E, M, K, N, T))
+        return launch_moe_gemm_down(w, dtype, E, M, K, N, T, ids, weights, H, residual, Y, work, st);
 #define QMM_CALL(DT)                                                                                                  \
     hipLaunchKernelGGL((moe_down_rows_kernel<DT>), dim3(rows_grid(N *M)), dim3(256), 0, st, (const uint8_t *)w, (int)E, \
                        M, K, N, (int)T, ids, weights, H, residual, Y)
