@@ -61,7 +61,7 @@ QMM_ARGMAX_WORK_BYTES = 32768
 QMM_NOALLOC_SCRATCH_BYTES = 32768
 QMM_READ_PROBE_OUT_FLOATS = 4096
 QMM_ROUTE_SOFTMAX, QMM_ROUTE_SIGMOID = 0, 1
-QMM_MOE_MAX_EXPERTS, QMM_MOE_MAX_TOPK = 1024, 32
+QMM_MOE_MAX_EXPERTS, QMM_MOE_MAX_TOPK, QMM_MOE_MAX_ROWS, QMM_MOE_MAX_K = 1024, 32, 4194304, 1048576
 
 EXPORTS = ("qmm_gemv", "qmm_gemv_concat", "qmm_gemv_swiglu", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_gemm", "qmm_gemm_swiglu",
            "qmm_quantize_q8_0", "qmm_gemm_q8act", "qmm_gemv_q8act", "qmm_gemv_concat_q8act",

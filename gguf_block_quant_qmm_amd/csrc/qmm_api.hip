@@ -149,12 +149,13 @@ int64_t mfma_from_n(int dtype, int64_t M, int64_t K) {
     return (dtype == QMM_Q4_0 || dtype == QMM_Q6_K) ? 3 : 2;
 }
 
-// Sizes of the routed experts' products: every index of a slot fits int32 and
-// every byte offset 63 bits.
+// Sizes of the routed experts' products: every index of a slot fits int32,
+// every byte offset 63 bits, a workgroup's rows 32 bits, every grid 2^32 threads.
 int check_moe(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
     const int rc = check_shape(dtype, M, K, N);
     if (rc != QMM_OK) return rc;
     if (E < 1 || E > QMM_MOE_MAX_EXPERTS || T < 1 || T > QMM_MOE_MAX_TOPK || N > INT32_MAX / T) return QMM_ERR_SHAPE;
+    if (M > QMM_MOE_MAX_ROWS || K > QMM_MOE_MAX_K) return QMM_ERR_SHAPE;
     constexpr int64_t kMaxProd = int64_t(1) << 56;
     if (M * K > kMaxProd / E || M > kMaxProd / (N * T) || K > kMaxProd / (N * T)) return QMM_ERR_SHAPE;
     return QMM_OK;

@@ -269,20 +269,6 @@ __device__ __forceinline__ void load_xa(const int8_t *xq, const float *xsc, int 
     }
 }
 
-// Activations go through LDS laid out so that the 16 lanes of a read phase,
-// each reading its own unit, hit distinct banks:
-//   PAD    one float4 of padding after every 16 (17 float4s per 64 values):
-//          a lane's 16 reads are one base address plus constant offsets
-//          (whole-row wavefronts, 272 bytes per unit);
-//   else   the float4 index XOR-swizzled within groups of 16 (256 bytes per
-//          unit; per-read address arithmetic).
-template <bool PAD>
-__device__ __forceinline__ int xslot(int f) {
-    if constexpr (PAD) return f + (f >> 4);
-    else return (f & ~15) | ((f & 15) ^ ((f >> 4) & 15));
-}
-constexpr size_t xs_unit_bytes(bool pad) { return pad ? 272 : 256; }
-
 // The activations are fetched into registers before any weight load is
 // issued and written to LDS afterwards: vector-memory loads return in order,
 // so fetching x after the weight prefetch would make the first product wait
@@ -310,21 +296,6 @@ __device__ __forceinline__ void store_x(const floatx4 (&r)[XPT], int U, floatx4 
     for (int i = 0; i < XPT; i++) {
         const int f = threadIdx.x + i * blockDim.x;
         xs[xslot<PAD>(f < last ? f : last)] = r[i];
-    }
-}
-
-// With PAD the offsets of a unit's float4s from its first one do not depend
-// on the lane: every unit layout starts at a multiple of 16 or at 4 more, and
-// its float4s lie at offsets o (< 28) with (first % 16) + (o % 16) < 16, so
-// xslot(first + o) = xslot(first) + o + o / 16.
-template <int DT, bool PAD>
-__device__ __forceinline__ void x_from_lds(const floatx4 *xs, int u, float (&xv)[64]) {
-    const int first = Unit<DT>::x4(u, 0);
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int o = Unit<DT>::x4(u, i) - first;
-        const floatx4 v = PAD ? xs[xslot<true>(first) + o + (o >> 4)] : xs[xslot<false>(Unit<DT>::x4(u, i))];
-        xv[4 * i] = v.x; xv[4 * i + 1] = v.y; xv[4 * i + 2] = v.z; xv[4 * i + 3] = v.w;
     }
 }
 

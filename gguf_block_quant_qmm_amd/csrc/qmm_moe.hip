@@ -1,6 +1,21 @@
 // qmm_moe.hip -- the routed experts' products (include/qmm.h, qmm_moe_swiglu
 // and qmm_moe_down): every token has T slots, slot (n, t) runs through expert
 // e = ids[n][t], and the experts' M x K matrices lie one after the other.
+//
+// Few tokens: the GEMV's f32 arithmetic (qmm_units.hpp), memory-bound on the
+// chosen experts' bytes.  Many tokens: the matrix cores (qmm_moe_gemm.hip).
+//
+// The few-token kernel cuts a row into units of 64 weights, one per lane, as
+// the GEMV does, but an expert's rows are often short (K of a few hundred
+// weights), so a row takes 16, 32 or 64 lanes and a wavefront 4, 2 or 1 rows at
+// once.  Rows longer than 4096 weights are cut into chunks.  An item is a
+// (slot, chunk) pair that a workgroup's rows need: the chunks of x for
+// gate/up, T times the chunks of the down rows.  A wavefront keeps its item's
+// activations in registers for all rows of the workgroup; the partial sums of
+// a row meet in LDS and are added in item order, so the down projection's sum
+// over a token's experts needs no second pass and no atomics.
+#include <algorithm>
+
 #include "qmm_device.hpp"
 #include "qmm_internal.hpp"
 #include "qmm_units.hpp"
@@ -9,97 +24,273 @@ namespace qmm {
 
 namespace {
 
-// One row of one expert against one activation row, a wavefront, any layout.
+// The last unit of a row with an odd number of 32-weight blocks holds one
+// block: what belongs to the next row is dropped.  A block of 18 or 34 bytes
+// ends inside a dword that may reach past the blob, where a bounds-checked
+// dword load gives 0, so its last two bytes come from a load of their own.
+template <int DT> constexpr bool has_tail = DT == QMM_Q4_0 || DT == QMM_Q8_0;
 template <int DT>
-__device__ __forceinline__ float row_dot(const uint8_t *row, const float *x, int64_t nb, int lane) {
-    float acc = 0.f;
-    for (int64_t b = lane; b < nb; b += 64) acc += block_dot_generic<DT>(row + b * Geo<DT>::BB, x + b * Geo<DT>::BS);
-    return wave_sum(acc);
-}
-
-template <int DT>
-__global__ void __launch_bounds__(256) moe_swiglu_rows_kernel(const uint8_t *gate, const uint8_t *up, int E, int64_t M,
-                                                              int64_t K, int64_t slots, int T, const int32_t *ids,
-                                                              const float *X, float *out) {
-    const int lane = (int)threadIdx.x & 63;
-    const int64_t nb = K / Geo<DT>::BS, row_bytes = nb * Geo<DT>::BB;
-    for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < slots * M; w += (int64_t)gridDim.x * 4) {
-        const int64_t slot = w / M, m = w % M;
-        const int e = ids[slot];
-        float v = 0.f;
-        if (e >= 0 && e < E) {
-            const int64_t at = ((int64_t)e * M + m) * row_bytes;
-            const float *x = X + slot / T * K;
-            v = silu(row_dot<DT>(gate + at, x, nb, lane)) * row_dot<DT>(up + at, x, nb, lane);
-        }
-        if (lane == 0) out[w] = v;
+__device__ __forceinline__ void keep_first_block(uint32_t (&v)[Unit<DT>::NL], uint32_t tail) {
+    constexpr int BB = Geo<DT>::BB;
+#pragma unroll
+    for (int i = 0; i < Unit<DT>::NL; i++) {
+        if (4 * i >= BB) v[i] = 0u;
+        else if (4 * i + 2 == BB) v[i] = tail;
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256) moe_down_rows_kernel(const uint8_t *w_blob, int E, int64_t M, int64_t K,
-                                                            int64_t N, int T, const int32_t *ids, const float *weights,
-                                                            const float *H, const float *residual, float *Y) {
-    const int lane = (int)threadIdx.x & 63;
-    const int64_t nb = K / Geo<DT>::BS, row_bytes = nb * Geo<DT>::BB;
-    for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < N * M; w += (int64_t)gridDim.x * 4) {
-        const int64_t n = w / M, m = w % M;
-        float y = residual ? residual[w] : 0.f;
-        for (int t = 0; t < T; t++) {
-            const int e = ids[n * T + t];
-            if (e < 0 || e >= E) continue;
-            const uint8_t *row = w_blob + ((int64_t)e * M + m) * row_bytes;
-            y = fmaf(weights[n * T + t], row_dot<DT>(row, H + (n * T + t) * K, nb, lane), y);
+template <int DT> struct UnitAt {  // a unit's byte offsets with the lane's row added
+    static __device__ typename Unit<DT>::Off of(int u, uint32_t row) {
+        typename Unit<DT>::Off o = Unit<DT>::lane_off(u);
+        if constexpr (DT == QMM_Q6_K) { o.a += row; o.c += row; o.s += row; o.d += row; }
+        else if constexpr (DT == QMM_Q4_K || DT == QMM_Q5_K) { o.hdr += row; o.qs += row; }
+        else o.a += row;
+        return o;
+    }
+};
+
+// The sum over the LPR lanes of a row, in its last lane.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+    if constexpr (LPR == 64) return wave_sum_to_lane63(v);
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, true));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xF, 0xF, true));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, true));
+    if constexpr (LPR == 32)
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xA, 0xF, false));
+    return v;
+}
+
+struct MoeGemvArgs {
+    const uint8_t *w0, *w1;    // swiglu: gate and up; down: w0
+    const int32_t *ids;
+    const float *weights, *residual, *x;
+    float *out;
+    int64_t M, K, row_bytes, mat_bytes;
+    int E, T, nb;              // nb: blocks per row
+    int U, C;                  // units per row, chunks of 64 units
+    int rows, rtiles;          // rows per workgroup, workgroups per matrix
+    int phases;                // wavefronts per item
+};
+
+// One workgroup: `rows` rows of one slot's expert (SWI), or of every expert of
+// one token.  W wavefronts; items round by round when there are more.
+// ODD: an odd number of 32-weight blocks per row.
+template <int DT, bool SWI, int LPR, bool ODD>
+__global__ void __launch_bounds__(512) moe_gemv_kernel(const MoeGemvArgs a) {
+    constexpr int RPW = 64 / LPR, NL = Unit<DT>::NL, NM = SWI ? 2 : 1;
+    constexpr int D = SWI ? 1 : 2;              // row groups in flight behind the current one
+    extern __shared__ __attribute__((aligned(16))) floatx4 xs[];
+    const int t = (int)threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int W = (int)blockDim.x >> 6;
+    const int items = SWI ? a.C : a.T * a.C, per_round = W / a.phases;
+    const int64_t job = blockIdx.x / a.rtiles;  // slot (SWI) or token
+    const int64_t row0 = (int64_t)(blockIdx.x % a.rtiles) * a.rows;
+    const int rows = (int)(a.M - row0 < a.rows ? a.M - row0 : a.rows);
+    // LDS: the activations of a round's items, then the partial sums [item of
+    // the round][matrix][row]
+    constexpr int XU = LPR * 17;                // float4 per item (padded units)
+    float *part = reinterpret_cast<float *>(xs + per_round * XU);
+
+    const int in_round = wave / a.phases, phase = wave % a.phases;
+    const int ul = lane % LPR, rl = lane / LPR;
+    const int groups = (rows + RPW - 1) / RPW;
+    if constexpr (SWI) {
+        const int e = a.ids[job];
+        if (e < 0 || e >= a.E) {                // uniform: no expert, zeros
+            for (int r = t; r < rows; r += (int)blockDim.x) a.out[job * a.M + row0 + r] = 0.f;
+            return;
         }
-        if (lane == 0) Y[w] = y;
+    }
+    for (int i0 = 0; i0 < items; i0 += per_round) {
+        const int item = i0 + in_round;
+        const int slot = SWI ? 0 : item / a.C, c = SWI ? item : item % a.C;
+        const bool have = in_round < per_round && item < items;
+        const int e = !have ? -1 : a.ids[SWI ? job : job * a.T + slot];
+        const bool live = e >= 0 && e < a.E;    // uniform per wavefront
+        const int u = 64 * c + ul;
+        const bool active = live && u < a.U;
+        const bool half = ODD && u == a.U - 1;
+        const int64_t at = (live ? (int64_t)e * a.mat_bytes : 0) + row0 * a.row_bytes;
+        const uint32_t mis = (uint32_t)(at & 3);
+        const uint32_t bytes = live ? (uint32_t)(rows * a.row_bytes) + mis : 0u;
+        const Rsrc rs[2] = {make_rsrc_uniform(a.w0 + (at - mis), bytes),
+                            make_rsrc_uniform((SWI ? a.w1 : a.w0) + (at - mis), bytes)};
+        const typename Unit<DT>::Off off = UnitAt<DT>::of(active ? u : 0, mis + (uint32_t)rl * (uint32_t)a.row_bytes);
+        uint32_t buf[D + 1][NM][NL], tail[D + 1][NM];
+        auto fetch = [&](int g, uint32_t (&b)[NM][NL], uint32_t (&tl)[NM]) {
+            const uint32_t so = (uint32_t)g * (uint32_t)(RPW * a.row_bytes);
+#pragma unroll
+            for (int m = 0; m < NM; m++) {
+                Unit<DT>::load(rs[m], so, off, b[m]);
+                if constexpr (ODD && has_tail<DT>)
+                    tl[m] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[m], off.a + (Geo<DT>::BB & ~3u), so, 0);
+                else tl[m] = 0u;
+            }
+        };
+        // activations first (loads return in order), then the first weights
+        constexpr int XR = LPR / 4;             // float4 per lane of an item's activations
+        floatx4 xr[XR];
+        const int64_t xrow = SWI ? job / a.T : job * a.T + slot;
+        const int64_t xleft = a.K - 4096 * (int64_t)c;
+        const Rsrc xrs = make_rsrc_uniform(a.x + xrow * a.K + 4096 * (int64_t)c,
+                                           live ? (uint32_t)(4 * (xleft < 4096 ? xleft : 4096)) : 0u);
+        const bool stage = phase == 0 && in_round < per_round;
+        if (stage) {                            // uniform per wavefront
+#pragma unroll
+            for (int i = 0; i < XR; i++)
+                xr[i] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(xrs, 16u * lane, 1024u * i, 0));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < D; s++) fetch(phase + s * a.phases, buf[s], tail[s]);
+        if (i0 > 0) __syncthreads();            // the round before is done with xs
+        if (stage) {
+#pragma unroll
+            for (int i = 0; i < XR; i++) xs[in_round * XU + xslot<true>(lane + 64 * i)] = xr[i];
+        }
+        __syncthreads();
+        float xv[64];
+        x_from_lds<DT, true>(xs + (in_round < per_round ? in_round : 0) * XU, active ? ul : 0, xv);
+        __builtin_amdgcn_sched_barrier(0);
+        float wt = 1.f;
+        if constexpr (!SWI) wt = live ? a.weights[job * a.T + slot] : 0.f;
+        const int mine = in_round < per_round ? groups : 0;
+        for (int g0 = phase; g0 < mine; g0 += (D + 1) * a.phases) {
+#pragma unroll
+            for (int s = 0; s <= D; s++) {
+                const int g = g0 + s * a.phases;
+                fetch(g + D * a.phases, buf[(s + D) % (D + 1)], tail[(s + D) % (D + 1)]);
+                if (g < mine) {                 // uniform per wavefront
+                    float v[NM];
+#pragma unroll
+                    for (int m = 0; m < NM; m++) {
+                        if (half) keep_first_block<DT>(buf[s][m], tail[s][m]);
+                        const float d = Unit<DT>::dot(buf[s][m], xv, off);
+                        v[m] = row_sum<LPR>(active ? d : 0.f);
+                    }
+                    const int r = g * RPW + rl;
+                    if (ul == LPR - 1 && r < rows) {
+#pragma unroll
+                        for (int m = 0; m < NM; m++) {
+                            // gate/up rounds add up in item order; the down sums of a
+                            // round's items are weighted here
+                            float *p = part + (in_round * NM + m) * a.rows + r;
+                            if constexpr (SWI) *p = i0 > 0 ? *p + v[m] : v[m];
+                            else if (live) *p = i0 > 0 ? fmaf(wt, v[m], *p) : wt * v[m];
+                            else if (i0 == 0) *p = 0.f;
+                        }
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int sums = items < per_round ? items : per_round;
+    for (int r = t; r < rows; r += (int)blockDim.x) {
+        if constexpr (SWI) {
+            float g = part[r], up = part[a.rows + r];
+            for (int i = 1; i < sums; i++) {
+                g += part[2 * i * a.rows + r];
+                up += part[(2 * i + 1) * a.rows + r];
+            }
+            a.out[job * a.M + row0 + r] = silu(g) * up;
+        } else {
+            float y = part[r];
+            for (int i = 1; i < sums; i++) y += part[i * a.rows + r];
+            const int64_t o = job * a.M + row0 + r;
+            a.out[o] = a.residual ? a.residual[o] + y : y;
+        }
     }
 }
 
-unsigned rows_grid(int64_t rows) {
-    const int64_t g = (rows + 3) / 4;
-    return (unsigned)(g < (1 << 20) ? g : (1 << 20));
+template <int DT, bool SWI, bool ODD>
+void launch_lpr(int lpr, dim3 grid, dim3 block, size_t lds, hipStream_t st, const MoeGemvArgs &a) {
+    switch (lpr) {
+    case 16: hipLaunchKernelGGL((moe_gemv_kernel<DT, SWI, 16, ODD>), grid, block, lds, st, a); break;
+    case 32: hipLaunchKernelGGL((moe_gemv_kernel<DT, SWI, 32, ODD>), grid, block, lds, st, a); break;
+    default: hipLaunchKernelGGL((moe_gemv_kernel<DT, SWI, 64, ODD>), grid, block, lds, st, a); break;
+    }
+}
+
+template <int DT, bool SWI>
+hipError_t run_gemv(const void *w0, const void *w1, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, const int32_t *ids,
+                    const float *weights, const float *x, const float *residual, float *out, hipStream_t st, int cus) {
+    MoeGemvArgs a;
+    a.w0 = static_cast<const uint8_t *>(w0);
+    a.w1 = static_cast<const uint8_t *>(w1);
+    a.ids = ids;
+    a.weights = weights;
+    a.residual = residual;
+    a.x = x;
+    a.out = out;
+    a.M = M;
+    a.K = K;
+    a.nb = (int)(K / Geo<DT>::BS);
+    a.row_bytes = (int64_t)a.nb * Geo<DT>::BB;
+    a.mat_bytes = M * a.row_bytes;
+    a.E = (int)E;
+    a.T = (int)T;
+    a.U = (int)((K + 63) / 64);
+    a.C = (a.U + 63) / 64;
+    const int lpr = a.U <= 16 ? 16 : (a.U <= 32 ? 32 : 64);
+    const int items = SWI ? a.C : (int)T * a.C;
+    // up to 8 wavefronts; several per item when there are few items
+    const int per_round = std::min(items, 8);
+    a.phases = items == 1 ? 4 : std::max(1, 8 / per_round);
+    const int W = per_round * a.phases, rpw = 64 / lpr;
+    const int64_t jobs = SWI ? N * T : N;
+    // rows per workgroup: about 16 wavefronts per CU (8 where every wavefront
+    // stages activations of its own), whole row groups for every phase
+    const int64_t wgs = std::max<int64_t>(1, (int64_t)cus * (items == 1 ? 16 : 8) / W);
+    const int64_t step = (int64_t)rpw * a.phases;
+    int64_t rows = (M * jobs + wgs - 1) / wgs;
+    rows = std::max(step, (rows + step - 1) / step * step);
+    rows = std::min<int64_t>(rows, std::max<int64_t>(step, 256 / step * step));
+    a.rows = (int)rows;
+    const int64_t rtiles = (M + rows - 1) / rows;
+    a.rtiles = (int)rtiles;
+    const size_t lds = (size_t)per_round * ((size_t)lpr * 272 + (SWI ? 2 : 1) * 4 * (size_t)rows);
+    const dim3 grid((unsigned)(jobs * rtiles)), block(64 * W);
+    if (Geo<DT>::BS == 32 && (a.nb & 1)) launch_lpr<DT, SWI, Geo<DT>::BS == 32>(lpr, grid, block, lds, st, a);
+    else launch_lpr<DT, SWI, false>(lpr, grid, block, lds, st, a);
+    return hipGetLastError();
+}
+
+// Few tokens run the GEMV form.  A tuning lever of measurement builds only.
+bool use_gemm(int64_t N) {
+    static const int lever = tuning_lever("QMM_MOE_GEMM_FROM_N", 8);
+    return N >= lever;
 }
 
 }  // namespace
 
-// Few tokens: a wavefront per row.  A tuning lever of measurement builds only.
-static bool use_gemm(int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
-    static const int lever = tuning_lever("QMM_MOE_GEMM_FROM_N", 8);
-    (void)E;
-    (void)T;
-    return moe_gemm_ok(M, K) && N >= lever;
-}
-
 int64_t moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
-    return use_gemm(E, M, K, N, T) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, false) : 0;
+    return use_gemm(N) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, false) : 0;
 }
 int64_t moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
-    return use_gemm(E, M, K, N, T) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, true) : 0;
+    return use_gemm(N) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, true) : 0;
 }
 
 hipError_t launch_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N,
                              int64_t T, const int32_t *ids, const float *X, float *out, void *work, hipStream_t st,
-                             int) {
-    if (use_gemm(E, M, K, N, T)) return launch_moe_gemm_swiglu(gate, up, dtype, E, M, K, N, T, ids, X, out, work, st);
-#define QMM_CALL(DT)                                                                                                   \
-    hipLaunchKernelGGL((moe_swiglu_rows_kernel<DT>), dim3(rows_grid(N *T *M)), dim3(256), 0, st, (const uint8_t *)gate, \
-                       (const uint8_t *)up, (int)E, M, K, N *T, (int)T, ids, X, out)
+                             int cus) {
+    if (use_gemm(N)) return launch_moe_gemm_swiglu(gate, up, dtype, E, M, K, N, T, ids, X, out, work, st);
+#define QMM_CALL(DT) return run_gemv<DT, true>(gate, up, E, M, K, N, T, ids, nullptr, X, nullptr, out, st, cus)
     QMM_MOE_DT(dtype, QMM_CALL)
 #undef QMM_CALL
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T,
                            const int32_t *ids, const float *weights, const float *H, const float *residual, float *Y,
-                           void *work, hipStream_t st, int) {
-    if (use_gemm(E, M, K, N, T))
-        return launch_moe_gemm_down(w, dtype, E, M, K, N, T, ids, weights, H, residual, Y, work, st);
-#define QMM_CALL(DT)                                                                                                  \
-    hipLaunchKernelGGL((moe_down_rows_kernel<DT>), dim3(rows_grid(N *M)), dim3(256), 0, st, (const uint8_t *)w, (int)E, \
-                       M, K, N, (int)T, ids, weights, H, residual, Y)
+                           void *work, hipStream_t st, int cus) {
+    if (use_gemm(N)) return launch_moe_gemm_down(w, dtype, E, M, K, N, T, ids, weights, H, residual, Y, work, st);
+#define QMM_CALL(DT) return run_gemv<DT, false>(w, nullptr, E, M, K, N, T, ids, weights, H, residual, Y, st, cus)
     QMM_MOE_DT(dtype, QMM_CALL)
 #undef QMM_CALL
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 }  // namespace qmm

@@ -675,9 +675,6 @@ MoeSizes moe_sizes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_
     return z;
 }
 
-// 32-bit offsets: a wavefront's 64 rows and a chunk of one token
-constexpr int64_t MOE_GEMM_K_MAX = int64_t(1) << 20, MOE_GEMM_M_MAX = int64_t(1) << 20;
-
 template <int DT, int FN, int W, bool SWI>
 void launch_gemm(const MoeGemmArgs &a, int64_t tiles, hipStream_t st) {
     const int64_t blocks = (tiles * a.mtiles + 7) / 8 * 8;
@@ -727,8 +724,6 @@ hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_
 
 // Slots per tile: 32 while an expert sees few of them, else 64.
 int moe_gemm_bn(int64_t E, int64_t N, int64_t T) { return N * T <= 32 * E ? 32 : 64; }
-
-bool moe_gemm_ok(int64_t M, int64_t K) { return M <= MOE_GEMM_M_MAX && K <= MOE_GEMM_K_MAX; }
 
 int64_t moe_gemm_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, bool down) {
     return moe_sizes(dtype, E, M, K, N, T, moe_gemm_bn(E, N, T), down).bytes;

@@ -390,6 +390,8 @@ int qmm_block_norm(const float *block, const float *w_post, const float *gate, i
 #define QMM_ROUTE_SIGMOID 1
 #define QMM_MOE_MAX_EXPERTS 1024
 #define QMM_MOE_MAX_TOPK 32
+#define QMM_MOE_MAX_ROWS 4194304
+#define QMM_MOE_MAX_K 1048576
 int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, int scoring, int64_t groups,
                   int64_t topk_groups, int group_top, int64_t topk, int renorm, float scale, int32_t *ids,
                   float *weights, void *stream);
@@ -411,7 +413,8 @@ int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, 
  *             in time (two streams, two captured graphs) need separate work.
  * Both projections are f32 class for every N: with S the sum of |w x|
  * of a projection, |error| <= 1e-5 * S.  1 <= E <= QMM_MOE_MAX_EXPERTS,
- * 1 <= T <= QMM_MOE_MAX_TOPK, N * T <= 2^31 - 1, any K the dtype allows. */
+ * 1 <= T <= QMM_MOE_MAX_TOPK, N * T <= 2^31 - 1, M <= QMM_MOE_MAX_ROWS, K any
+ * multiple of the block size up to QMM_MOE_MAX_K. */
 int64_t qmm_moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
 int qmm_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T,
                    const int32_t *ids, const float *X, float *out, void *work, int64_t work_bytes, void *stream);
