@@ -78,9 +78,12 @@ struct MoeGemvArgs {
 // one token.  W wavefronts; items round by round when there are more.
 // ODD: an odd number of 32-weight blocks per row.
 template <int DT, bool SWI, int LPR, bool ODD>
-__global__ void __launch_bounds__(512) moe_gemv_kernel(const MoeGemvArgs a) {
+#ifndef GV_OCC
+#define GV_OCC 2
+#endif
+__global__ void __launch_bounds__(512, GV_OCC) moe_gemv_kernel(const MoeGemvArgs a) {
     constexpr int RPW = 64 / LPR, NL = Unit<DT>::NL, NM = SWI ? 2 : 1;
-    constexpr int D = SWI ? 1 : 2;              // row groups in flight behind the current one
+    constexpr int D = 3 * NM * NL <= 60 ? 2 : 1;  // row groups in flight behind the current one
     extern __shared__ __attribute__((aligned(16))) floatx4 xs[];
     const int t = (int)threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int W = (int)blockDim.x >> 6;
@@ -107,6 +110,19 @@ __global__ void __launch_bounds__(512) moe_gemv_kernel(const MoeGemvArgs a) {
         const int item = i0 + in_round;
         const int slot = SWI ? 0 : item / a.C, c = SWI ? item : item % a.C;
         const bool have = in_round < per_round && item < items;
+        // activations first: loads return in order, and they need no expert id
+        constexpr int XR = LPR / 4;             // float4 per lane of an item's activations
+        floatx4 xr[XR];
+        const int64_t xrow = SWI ? job / a.T : job * a.T + slot;
+        const int64_t xleft = a.K - 4096 * (int64_t)c;
+        const Rsrc xrs = make_rsrc_uniform(a.x + xrow * a.K + 4096 * (int64_t)c,
+                                           have ? (uint32_t)(4 * (xleft < 4096 ? xleft : 4096)) : 0u);
+        const bool stage = phase == 0 && in_round < per_round;
+        if (stage) {                            // uniform per wavefront
+#pragma unroll
+            for (int i = 0; i < XR; i++)
+                xr[i] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(xrs, 16u * lane, 1024u * i, 0));
+        }
         const int e = !have ? -1 : a.ids[SWI ? job : job * a.T + slot];
         const bool live = e >= 0 && e < a.E;    // uniform per wavefront
         const int u = 64 * c + ul;
@@ -129,19 +145,6 @@ __global__ void __launch_bounds__(512) moe_gemv_kernel(const MoeGemvArgs a) {
                 else tl[m] = 0u;
             }
         };
-        // activations first (loads return in order), then the first weights
-        constexpr int XR = LPR / 4;             // float4 per lane of an item's activations
-        floatx4 xr[XR];
-        const int64_t xrow = SWI ? job / a.T : job * a.T + slot;
-        const int64_t xleft = a.K - 4096 * (int64_t)c;
-        const Rsrc xrs = make_rsrc_uniform(a.x + xrow * a.K + 4096 * (int64_t)c,
-                                           live ? (uint32_t)(4 * (xleft < 4096 ? xleft : 4096)) : 0u);
-        const bool stage = phase == 0 && in_round < per_round;
-        if (stage) {                            // uniform per wavefront
-#pragma unroll
-            for (int i = 0; i < XR; i++)
-                xr[i] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(xrs, 16u * lane, 1024u * i, 0));
-        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < D; s++) fetch(phase + s * a.phases, buf[s], tail[s]);
@@ -243,9 +246,12 @@ hipError_t run_gemv(const void *w0, const void *w1, int64_t E, int64_t M, int64_
     const int64_t jobs = SWI ? N * T : N;
     // rows per workgroup: about 16 wavefronts per CU (8 where every wavefront
     // stages activations of its own), whole row groups for every phase
-    const int64_t wgs = std::max<int64_t>(1, (int64_t)cus * (items == 1 ? 16 : 8) / W);
+    static const int wpc_lever = tuning_lever("QMM_MOE_GEMV_WPC", 0);
+    const int wpc = wpc_lever ? wpc_lever : (items == 1 ? 16 : 8);
+    const int64_t wgs = std::max<int64_t>(1, (int64_t)cus * wpc / W);
     const int64_t step = (int64_t)rpw * a.phases;
-    int64_t rows = (M * jobs + wgs - 1) / wgs;
+    const int64_t tiles_max = std::max<int64_t>(1, wgs / jobs);  // no last, nearly empty round of workgroups
+    int64_t rows = (M + tiles_max - 1) / tiles_max;
     rows = std::max(step, (rows + step - 1) / step * step);
     rows = std::min<int64_t>(rows, std::max<int64_t>(step, 256 / step * step));
     a.rows = (int)rows;

@@ -29,7 +29,8 @@ namespace qmm {
 namespace {
 
 constexpr int KT = 128;                 // weights of a row per k-tile
-constexpr int KT_BYTES = 4 * KT;        // a row's split activations of a k-tile: 128 hi, 128 lo
+constexpr int XT_BYTES = 2 * KT;        // a row's split activations of half a k-tile: 64 hi, 64 lo
+constexpr int KT_BYTES = 2 * XT_BYTES;
 constexpr int MOE_E_MAX = QMM_MOE_MAX_EXPERTS;
 
 // --------------------------------------------------------------- decoders ----
@@ -38,13 +39,16 @@ constexpr int MOE_E_MAX = QMM_MOE_MAX_EXPERTS;
 // the 8 weights kbase(2 s + kh) + sigma(j), sigma = (0 2 1 3 4 6 5 7): the
 // order in which a dword's bytes unpack pairwise.  The split activations are
 // written in the same order.
-//   NW          raw dwords per row and k-tile
+//   LP, TB      a k-tile's main bytes of a row: LP lanes x 16 bytes, row offset TB(kt)
+//   ROW         bytes a row's raw k-tile takes in LDS (a multiple of 16 whose
+//               dwords step through all banks: 16 rows' 16-byte reads never collide)
+//   Extra       the bytes of a row outside the main ones: loaded by the row's two
+//               lanes (kh = 0, 1), stored to LDS behind the main bytes
+//   NW          raw dwords per row and k-tile in registers
 //   STEPS       steps per chain (one scale); step(i): the i-th step to run
-//   NG          load groups: group g is used up by the steps i of its eighth
-//               ((i + 1) * NG / 8 > g for the first time), then reloaded with the
-//               next k-tile's bytes, so a row holds one k-tile of raw registers
+//   NG          groups of raw dwords, group g read from LDS while group g - 1 runs
 //   OFF         the format has block minima (offsets): one more step per tile
-//   load()      group g's bytes (row offset `row` in the resource, k-tile kt)
+//   read()      group g of a row from LDS
 //   scale()     the scale of the chain that step st ends; nb = blocks of 32 left in the row
 //   frag()      the weight operand of step st
 //   xscale(p)   factor on the activations of piece p (a power of two)
@@ -63,9 +67,23 @@ __device__ __forceinline__ half2v hi_code(uint32_t w, float bias) { return h2((w
 __device__ __forceinline__ half2v byte02_code(uint32_t w, float bias) { return bytes02_as_f16(w) - splat(1024.f + bias); }
 __device__ __forceinline__ half2v byte13_code(uint32_t w, float bias) { return bytes13_as_f16(w) - splat(1024.f + bias); }
 
-__device__ __forceinline__ uint32_t ld16(Rsrc rs, uint32_t off) { return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0); }
-__device__ __forceinline__ u32x2_t ld64(Rsrc rs, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0); }
-__device__ __forceinline__ u32x4_t ld128(Rsrc rs, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0); }
+__device__ __forceinline__ uint32_t ld16(Rsrc rs, uint32_t off, uint32_t so) { return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, off, so, 0); }
+__device__ __forceinline__ uint32_t ld32(Rsrc rs, uint32_t off, uint32_t so) { return __builtin_amdgcn_raw_buffer_load_b32(rs, off, so, 0); }
+__device__ __forceinline__ u32x2_t ld64(Rsrc rs, uint32_t off, uint32_t so) { return __builtin_amdgcn_raw_buffer_load_b64(rs, off, so, 0); }
+__device__ __forceinline__ u32x4_t ld128(Rsrc rs, uint32_t off, uint32_t so) { return __builtin_amdgcn_raw_buffer_load_b128(rs, off, so, 0); }
+__device__ __forceinline__ uint32_t at32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
+__device__ __forceinline__ uint32_t at16(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
+__device__ __forceinline__ u32x2_t at64(const uint8_t *p) { return *reinterpret_cast<const u32x2_t *>(p); }
+__device__ __forceinline__ u32x4_t at128(const uint8_t *p) { return *reinterpret_cast<const u32x4_t *>(p); }
+// 4 N bytes at p, a dword boundary or 2 past one
+template <int N, bool ODD>
+__device__ __forceinline__ void lds_dwords(const uint8_t *p, uint32_t *r) {
+    uint32_t w[N + 1];
+#pragma unroll
+    for (int i = 0; i < N + (ODD ? 1 : 0); i++) w[i] = at32(p - (ODD ? 2 : 0) + 4 * i);
+#pragma unroll
+    for (int i = 0; i < N; i++) r[i] = ODD ? __builtin_amdgcn_alignbyte(w[i + 1], w[i], 2) : w[i];
+}
 
 template <int DT> struct MDec;
 
@@ -80,11 +98,15 @@ template <> struct MDec<QMM_Q4_0> {
     __host__ __device__ static int kbase(int p) { return kbase_nibble(p); }
     __host__ __device__ static float xscale(int p) { return (p >> 1) & 1 ? 0.0625f : 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, int g, uint32_t (&r)[NW]) {
-        const uint32_t o = row + 72u * (uint32_t)kt + 18u * g;
-        const u32x2_t q = ld64(rs, o + 2u + 8u * kh);
-        r[3 * g] = q.x; r[3 * g + 1] = q.y;
-        r[3 * g + 2] = ld16(rs, o);
+    static constexpr int LP = 4, ROW = 80;
+    __device__ static uint32_t TB(int kt) { return 72u * (uint32_t)kt; }
+    struct Extra { uint32_t v; };  // bytes 64 .. 71
+    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) { x.v = ld32(rs, row + 64u + 4u * kh, TB(kt)); }
+    __device__ static void store(uint8_t *p, int kh, const Extra &x) { *reinterpret_cast<uint32_t *>(p + 64 + 4 * kh) = x.v; }
+    __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
+        if (g & 1) lds_dwords<2, false>(p + 18 * g + 2 + 8 * kh, &r[3 * g]);
+        else lds_dwords<2, true>(p + 18 * g + 2 + 8 * kh, &r[3 * g]);
+        r[3 * g + 2] = at16(p + 18 * g);
     }
     __device__ static void prep(const uint32_t (&)[NW], int, int, Pre &) {}
     __device__ static float scale(const uint32_t (&r)[NW], int st, int nb, const Pre &) { return (st >> 1) < nb ? h2f(r[3 * (st >> 1) + 2]) : 0.f; }
@@ -102,11 +124,14 @@ template <> struct MDec<QMM_Q4_1> {
     __host__ __device__ static int kbase(int p) { return kbase_nibble(p); }
     __host__ __device__ static float xscale(int p) { return (p >> 1) & 1 ? 0.0625f : 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, int g, uint32_t (&r)[NW]) {
-        const uint32_t o = row + 80u * (uint32_t)kt + 20u * g;
-        const u32x2_t q = ld64(rs, o + 4u + 8u * kh);
-        r[3 * g] = q.x; r[3 * g + 1] = q.y;
-        r[3 * g + 2] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
+    static constexpr int LP = 4, ROW = 80;
+    __device__ static uint32_t TB(int kt) { return 80u * (uint32_t)kt; }
+    struct Extra { u32x2_t v; };  // bytes 64 .. 79
+    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) { x.v = ld64(rs, row + 64u + 8u * kh, TB(kt)); }
+    __device__ static void store(uint8_t *p, int kh, const Extra &x) { *reinterpret_cast<u32x2_t *>(p + 64 + 8 * kh) = x.v; }
+    __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
+        lds_dwords<2, false>(p + 20 * g + 4 + 8 * kh, &r[3 * g]);
+        r[3 * g + 2] = at32(p + 20 * g);
     }
     __device__ static void prep(const uint32_t (&)[NW], int, int, Pre &) {}
     // also keeps the block's minimum: the four meet [S0 S2 S1 S3] hi and lo (lane half 0)
@@ -115,9 +140,9 @@ template <> struct MDec<QMM_Q4_1> {
         p.m[b] = b < nb ? r[3 * b + 2] >> 16 : 0u;
         return b < nb ? h2f(r[3 * b + 2]) : 0.f;
     }
-    __device__ static half8 offset(const Pre &p, float &so) {
+    static constexpr bool PAIR = false;  // every k-tile; the minima stand for themselves (scale 1)
+    __device__ static half8 offset(const uint32_t (&)[NW], int, const Pre &p, float &) {
         const half2v a = h2(p.m[0] | (p.m[2] << 16)), c = h2(p.m[1] | (p.m[3] << 16));
-        so = 1.f;
         return join(a, c, a, c);
     }
     __device__ static half8 frag(const uint32_t (&r)[NW], int st, int, const Pre &) {
@@ -135,11 +160,15 @@ template <> struct MDec<QMM_Q8_0> {
     __host__ __device__ static int kbase(int p) { return 32 * (p >> 2) + 16 * (p & 1) + 8 * ((p >> 1) & 1); }
     __host__ __device__ static float xscale(int) { return 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, int g, uint32_t (&r)[NW]) {
-        const uint32_t o = row + 136u * (uint32_t)kt + 34u * g;
-        const u32x4_t q = ld128(rs, o + 2u + 16u * kh);
-        r[5 * g] = q.x; r[5 * g + 1] = q.y; r[5 * g + 2] = q.z; r[5 * g + 3] = q.w;
-        r[5 * g + 4] = ld16(rs, o);
+    static constexpr int LP = 8, ROW = 144;
+    __device__ static uint32_t TB(int kt) { return 136u * (uint32_t)kt; }
+    struct Extra { uint32_t v; };  // bytes 128 .. 135
+    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) { x.v = ld32(rs, row + 128u + 4u * kh, TB(kt)); }
+    __device__ static void store(uint8_t *p, int kh, const Extra &x) { *reinterpret_cast<uint32_t *>(p + 128 + 4 * kh) = x.v; }
+    __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
+        if (g & 1) lds_dwords<4, false>(p + 34 * g + 2 + 16 * kh, &r[5 * g]);
+        else lds_dwords<4, true>(p + 34 * g + 2 + 16 * kh, &r[5 * g]);
+        r[5 * g + 4] = at16(p + 34 * g);
     }
     __device__ static void prep(const uint32_t (&)[NW], int, int, Pre &) {}
     __device__ static float scale(const uint32_t (&r)[NW], int st, int nb, const Pre &) { return (st >> 1) < nb ? h2f(r[5 * (st >> 1) + 4]) : 0.f; }
@@ -159,12 +188,13 @@ __host__ __device__ inline int kbase_k(int p) {
     const int st = p >> 1, kh = p & 1;
     return 64 * (st >> 2) + 32 * ((st >> 1) & 1) + 16 * kh + 8 * (st & 1);
 }
-// four 6-bit scales (or minima) of sub-blocks 4 t .. 4 t + 3, one per byte
-__device__ __forceinline__ uint32_t k_scales4(uint32_t s0, uint32_t s2, int t) {
-    return t ? ((s2 & 0x0F0F0F0Fu) | ((s0 >> 2) & 0x30303030u)) : (s0 & 0x3F3F3F3Fu);
+// four 6-bit scales (or minima) of sub-blocks 4 t .. 4 t + 3, one per byte; t is
+// 0 or ~0 (masks: a uniform branch per dword costs more than both sides)
+__device__ __forceinline__ uint32_t k_scales4(uint32_t s0, uint32_t s2, uint32_t t) {
+    return (s0 & 0x3F3F3F3Fu & ~t) | (((s2 & 0x0F0F0F0Fu) | ((s0 >> 2) & 0x30303030u)) & t);
 }
-__device__ __forceinline__ uint32_t k_mins4(uint32_t s1, uint32_t s2, int t) {
-    return t ? (((s2 >> 4) & 0x0F0F0F0Fu) | ((s1 >> 2) & 0x30303030u)) : (s1 & 0x3F3F3F3Fu);
+__device__ __forceinline__ uint32_t k_mins4(uint32_t s1, uint32_t s2, uint32_t t) {
+    return (s1 & 0x3F3F3F3Fu & ~t) | ((((s2 >> 4) & 0x0F0F0F0Fu) | ((s1 >> 2) & 0x30303030u)) & t);
 }
 template <int QH>
 struct MDecK {
@@ -172,38 +202,51 @@ struct MDecK {
     static constexpr bool OFF = true;
     struct Pre {
         half2v a, b;  // sc of sub-blocks (0, 2) times 2^10 and (1, 3) times 2^6
-        half2v m, n;  // minima of sub-blocks (0, 2) and (1, 3)
-        float d, dmin;
+        float d;
     };
     __host__ __device__ static int kbase(int p) { return kbase_k(p); }
     __host__ __device__ static float xscale(int) { return 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, int g, uint32_t (&r)[NW]) {
-        const uint32_t o = row + (uint32_t)BB * (uint32_t)(kt >> 1);
-        const u32x4_t q = ld128(rs, o + 16u + 32u * QH + 64u * (kt & 1) + 32u * g + 16u * kh);
+    // LDS row: the 64 code bytes of the half super-block, qh[32] (Q5_K), the header
+    static constexpr int LP = 4, ROW = QH ? 112 : 80;
+    __device__ static uint32_t TB(int kt) { return (uint32_t)BB * (uint32_t)(kt >> 1) + 16u + 32u * QH + 64u * (kt & 1); }
+    struct Extra { u32x2_t h; u32x4_t q; };
+    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) {
+        const uint32_t sb = (uint32_t)BB * (uint32_t)(kt >> 1);
+        x.h = ld64(rs, row + 8u * kh, sb);
+        if constexpr (QH) x.q = ld128(rs, row + 16u + 16u * kh, sb);
+    }
+    __device__ static void store(uint8_t *p, int kh, const Extra &x) {
+        *reinterpret_cast<u32x2_t *>(p + ROW - 16 + 8 * kh) = x.h;
+        if constexpr (QH) *reinterpret_cast<u32x4_t *>(p + 64 + 16 * kh) = x.q;
+    }
+    __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
+        const u32x4_t q = at128(p + 32 * g + 16 * kh);
         r[4 + 4 * g] = q.x; r[5 + 4 * g] = q.y; r[6 + 4 * g] = q.z; r[7 + 4 * g] = q.w;
         if (g == 0) {
-            const u32x4_t h = ld128(rs, o);
+            const u32x4_t h = at128(p + ROW - 16);
             r[0] = h.x; r[1] = h.y; r[2] = h.z; r[3] = h.w;
-        }
-        if (QH && g == 1) {
-            const u32x4_t b = ld128(rs, o + 16u + 16u * kh);
-            r[NW - 4] = b.x; r[NW - 3] = b.y; r[NW - 2] = b.z; r[NW - 1] = b.w;
+            if constexpr (QH) {
+                const u32x4_t b = at128(p + 64 + 16 * kh);
+                r[NW - 4] = b.x; r[NW - 3] = b.y; r[NW - 2] = b.z; r[NW - 1] = b.w;
+            }
         }
     }
     __device__ static void prep(const uint32_t (&r)[NW], int kt, int, Pre &p) {
-        const uint32_t sc = k_scales4(r[1], r[3], kt & 1), mn = k_mins4(r[2], r[3], kt & 1);
+        const uint32_t sc = k_scales4(r[1], r[3], (uint32_t)-(kt & 1));
         p.a = byte02_code(sc, 0.f) * splat(1024.f);
         p.b = byte13_code(sc, 0.f) * splat(64.f);
-        p.m = byte02_code(mn, 0.f);
-        p.n = byte13_code(mn, 0.f);
         p.d = h2f(r[0]) * 16384.f;
-        p.dmin = -h2f(r[0] >> 16);
     }
     __device__ static float scale(const uint32_t (&)[NW], int, int, const Pre &p) { return p.d; }
-    __device__ static half8 offset(const Pre &p, float &so) {
-        so = p.dmin;
-        return join(p.m, p.n, p.m, p.n);
+    // the minima of the whole super-block in one step, after its second k-tile:
+    // lane half kh holds those of k-tile kh
+    static constexpr bool PAIR = true;
+    __device__ static half8 offset(const uint32_t (&r)[NW], int kh, const Pre &, float &so) {
+        const uint32_t mn = k_mins4(r[2], r[3], (uint32_t)-kh);
+        so = -h2f(r[0] >> 16);
+        const half2v m = byte02_code(mn, 0.f), n = byte13_code(mn, 0.f);  // [m0 m2], [m1 m3]
+        return join(m, n, m, n);
     }
     __device__ static half8 frag(const uint32_t (&r)[NW], int st, int kt, const Pre &p) {
         const int c = st >> 2, hi = (st >> 1) & 1, i = 4 + 4 * c + 2 * (st & 1);
@@ -233,18 +276,31 @@ template <> struct MDec<QMM_Q6_K> {
     static constexpr int NW = 15, STEPS = 1, NG = 2;
     static constexpr bool OFF = false;
     struct Pre { float s[8]; };
-    __host__ __device__ static int kbase(int p) { return 8 * p; }
-    __host__ __device__ static float xscale(int) { return 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return 2 * (i & 3) + (i >> 2); }
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, int g, uint32_t (&r)[NW]) {
-        const uint32_t o = row + 210u * (uint32_t)(kt >> 1), h = kt & 1;
-        const u32x2_t a = ld64(rs, o + 64u * h + 16u * g + 8u * kh), b = ld64(rs, o + 64u * h + 32u + 16u * g + 8u * kh);
-        const u32x2_t c = ld64(rs, o + 128u + 32u * h + 16u * g + 8u * kh);
+    __host__ __device__ static int kbase(int p) { return 16 * step(p >> 1) + 8 * (p & 1); }
+    __host__ __device__ static float xscale(int) { return 1.0f; }
+    // LDS row: ql[64] of the half, qh[32], the 8 sub-scales, d
+    static constexpr int LP = 4, ROW = 112;
+    __device__ static uint32_t TB(int kt) { return 210u * (uint32_t)(kt >> 1) + 64u * (kt & 1); }
+    struct Extra { u32x4_t q; uint32_t sc, d; };
+    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) {
+        const uint32_t sb = 210u * (uint32_t)(kt >> 1), h = kt & 1;
+        x.q = ld128(rs, row + 128u + 16u * kh, sb + 32u * h);
+        x.sc = ld32(rs, row + 192u + 4u * kh, sb + 8u * h);
+        x.d = ld16(rs, row + 208u, sb);
+    }
+    __device__ static void store(uint8_t *p, int kh, const Extra &x) {
+        *reinterpret_cast<u32x4_t *>(p + 64 + 16 * kh) = x.q;
+        *reinterpret_cast<uint32_t *>(p + 96 + 4 * kh) = x.sc;
+        *reinterpret_cast<uint32_t *>(p + 104 + 4 * kh) = x.d;  // both lanes: a branch here costs registers
+    }
+    __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
+        const u32x2_t a = at64(p + 16 * g + 8 * kh), b = at64(p + 32 + 16 * g + 8 * kh), c = at64(p + 64 + 16 * g + 8 * kh);
         r[6 * g] = a.x; r[6 * g + 1] = a.y; r[6 * g + 2] = b.x; r[6 * g + 3] = b.y; r[6 * g + 4] = c.x; r[6 * g + 5] = c.y;
         if (g == 0) {
-            const u32x2_t sc = ld64(rs, o + 192u + 8u * h);
+            const u32x2_t sc = at64(p + 96);
             r[12] = sc.x; r[13] = sc.y;
-            r[14] = ld16(rs, o + 208u);
+            r[14] = at32(p + 104);
         }
     }
     __device__ static void prep(const uint32_t (&r)[NW], int, int, Pre &p) {
@@ -267,14 +323,15 @@ template <> struct MDec<QMM_Q6_K> {
 };
 
 // ------------------------------------------------------------- preparation ----
-// The workspace of one call (see moe_ws).  tiles[0].x = number of tiles; tile i
-// is tiles[1 + i] = (expert, first position in order, rows, 0).
+// The workspace of one call.  tiles[0].x = number of tiles; tile i is tiles[1 +
+// i] = (expert, first position in order, rows | tiles of the expert << 8, first
+// tile of the expert).
 struct MoeWs {
     int4 *tiles;
     int32_t *order;   // the slots, expert after expert
     float *rscale;    // per row: what the split row was divided by
     uint4 *sums;      // [row][k-tile]: 4 block sums, hi and lo (formats with minima)
-    uint8_t *xs;      // [row][k-tile][KT_BYTES]
+    uint8_t *xs;      // [row][half k-tile][hi, lo][8 pieces of 8 values]
     float *prod;      // down: [slot][M]
 };
 
@@ -314,7 +371,7 @@ __device__ void plan_tiles(const int32_t *ids, int S, int E, int BN, int4 *tiles
     for (int e = t; e < E; e += T) {
         const int c = count[e];
         for (int i = 0; i * BN < c; i++)
-            tiles[1 + tile0[e] + i] = int4{e, start[e] + i * BN, c - i * BN < BN ? c - i * BN : BN, 0};
+            tiles[1 + tile0[e] + i] = int4{e, start[e] + i * BN, (c - i * BN < BN ? c - i * BN : BN) | ((c + BN - 1) / BN) << 8, tile0[e]};
     }
     __syncthreads();
     for (int s = t; s < S; s += T) {
@@ -323,88 +380,117 @@ __device__ void plan_tiles(const int32_t *ids, int S, int E, int BN, int4 *tiles
     }
 }
 
-// Blocks 1 ..: one activation row each (rows of a slot without an expert are
-// skipped where skip_ids is given).  Threads hold 8 values per piece.
+// One piece (8 values, in the operand order) of a split row: 16 bytes of hi, 16 of lo.
 template <int DT>
-__global__ void __launch_bounds__(256) moe_prep_kernel(const int32_t *ids, int S, int E, int BN, MoeWs ws, const float *X,
-                                                       int64_t rows, int K, int nkt, int per_row_ids) {
+__device__ __forceinline__ void put_piece(const MoeWs &ws, int64_t row, int nkt, int i, const floatx4 &a, const floatx4 &b, float mul) {
+    const int kt = i >> 4, p = i & 15;
+    const float f = mul * MDec<DT>::xscale(p);
+    const float v[8] = {a.x, a.z, a.y, a.w, b.x, b.z, b.y, b.w};
+    half8 hi, lo;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float s = v[j] * f;
+        sum += mul * v[j];
+        hi[j] = (_Float16)s;
+        const float r = s - (float)hi[j];
+        lo[j] = (_Float16)(r == r ? r : 0.f);  // a non-finite x is in hi alone
+    }
+    half8 *o8 = reinterpret_cast<half8 *>(ws.xs + (row * nkt + kt) * (int64_t)KT_BYTES + (p >> 3) * XT_BYTES);
+    o8[p & 7] = hi;
+    o8[8 + (p & 7)] = lo;
+    if constexpr (MDec<DT>::OFF) {
+        // block b of the k-tile is pieces 4b .. 4b + 3: four neighbouring lanes
+        sum += __shfl_xor(sum, 1, 64);
+        sum += __shfl_xor(sum, 2, 64);
+        const int l = (int)threadIdx.x & 48;
+        const float s[4] = {__shfl(sum, l, 64), __shfl(sum, l + 8, 64), __shfl(sum, l + 4, 64), __shfl(sum, l + 12, 64)};
+        if (p == 0) {
+            half8 o;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                o[j] = (_Float16)s[j];
+                const float r = s[j] - (float)o[j];
+                o[4 + j] = (_Float16)(r == r ? r : 0.f);
+            }
+            ws.sums[row * nkt + kt] = __builtin_bit_cast(uint4, o);
+        }
+    }
+}
+
+// Workgroup 0 plans the tiles; a wavefront of the others splits one row.  REG:
+// the row (up to 4096 values) stays in registers between the maximum and the
+// split; else it is read twice.  zero_out (gate/up): the output rows [M] of a
+// token's slots without an expert are cleared here, for the GEMM writes only
+// rows that have one.  slot_rows (down): rows are slots, and those without an
+// expert are skipped.
+template <int DT, bool REG>
+__global__ void __launch_bounds__(512) moe_prep_kernel(const int32_t *ids, int S, int E, int BN, MoeWs ws, const float *X,
+                                                       int64_t rows, int K, int nkt, int T, bool slot_rows, float *zero_out,
+                                                       int64_t M) {
     if (blockIdx.x == 0) {
         plan_tiles(ids, S, E, BN, ws.tiles, ws.order);
         return;
     }
-    const int64_t row = (int64_t)blockIdx.x - 1;
-    if (per_row_ids) {
+    const int lane = (int)threadIdx.x & 63;
+    const int64_t row = ((int64_t)blockIdx.x - 1) * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    if (row >= rows) return;
+    if (slot_rows) {
         const int e = ids[row];
         if (e < 0 || e >= E) return;
+    } else {
+        for (int t = 0; t < T; t++) {
+            const int e = ids[row * T + t];
+            if (e < 0 || e >= E)
+                for (int64_t m = lane; m < M; m += 64) zero_out[(row * T + t) * M + m] = 0.f;
+        }
     }
-    const float *x = X + row * K;
-    const int t = (int)threadIdx.x, T = (int)blockDim.x;
-    __shared__ float red[4];
+    const int n = nkt * 16;  // pieces; lanes of a 16-lane group are in or out together
+    const Rsrc rs = make_rsrc_uniform(X + row * K, 4u * (uint32_t)K);  // zeros past the row
     float amax = 0.f;
-    for (int i = t; i < K / 4; i += T) {  // K % 32 == 0
-        const floatx4 v = reinterpret_cast<const floatx4 *>(x)[i];
+    auto fold = [&](const floatx4 &v) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const float a = fabsf(v[j]);
             amax = (a > amax && a < __builtin_inff()) ? a : amax;
         }
+    };
+    auto load = [&](int i, floatx4 &a, floatx4 &b) {
+        const uint32_t k = 4u * (uint32_t)((i >> 4) * KT + MDec<DT>::kbase(i & 15));
+        a = __builtin_bit_cast(floatx4, ld128(rs, k, 0));
+        b = __builtin_bit_cast(floatx4, ld128(rs, k + 16u, 0));
+    };
+    constexpr int PPL = REG ? 8 : 1;
+    floatx4 va[PPL], vb[PPL];
+    if constexpr (REG) {
+#pragma unroll
+        for (int j = 0; j < PPL; j++) load(lane + 64 * j, va[j], vb[j]);
+#pragma unroll
+        for (int j = 0; j < PPL; j++) { fold(va[j]); fold(vb[j]); }
+    } else {
+        for (int i = lane; i < n; i += 64) {
+            load(i, va[0], vb[0]);
+            fold(va[0]);
+            fold(vb[0]);
+        }
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
-    if ((t & 63) == 0) red[t >> 6] = amax;
-    __syncthreads();
-    amax = red[0];
-    for (int w = 1; w < T / 64; w++) amax = fmaxf(amax, red[w]);
     // amax = f * 2^e, f in [0.5, 1): multiply by 2^(10 - e)
     int e = 0;
     (void)frexpf(amax, &e);
     int m = amax > 0.f ? 10 - e : 0;
     m = m > 126 ? 126 : m;
     const float mul = ldexpf(1.0f, m);
-    if (t == 0) ws.rscale[row] = ldexpf(1.0f, -m);
-    uint8_t *dst = ws.xs + row * (int64_t)nkt * KT_BYTES;
-    for (int i = t; i < nkt * 16; i += T) {
-        const int kt = i >> 4, p = i & 15, k = kt * KT + MDec<DT>::kbase(p);
-        const float f = mul * MDec<DT>::xscale(p);
-        float v[8];
-        float sum = 0.f;
-        if (k < K) {  // whole pieces: K % 32 == 0
-            const floatx4 a = *reinterpret_cast<const floatx4 *>(x + k), b = *reinterpret_cast<const floatx4 *>(x + k + 4);
-            v[0] = a.x; v[1] = a.z; v[2] = a.y; v[3] = a.w; v[4] = b.x; v[5] = b.z; v[6] = b.y; v[7] = b.w;
+    if (lane == 0) ws.rscale[row] = ldexpf(1.0f, -m);
+    if constexpr (REG) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) sum += mul * v[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = 0.f;
-        }
-        half8 hi, lo;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float s = v[j] * f;
-            hi[j] = (_Float16)s;
-            const float r = s - (float)hi[j];
-            lo[j] = (_Float16)(r == r ? r : 0.f);  // a non-finite x is in hi alone
-        }
-        reinterpret_cast<half8 *>(dst + (int64_t)kt * KT_BYTES)[p] = hi;
-        reinterpret_cast<half8 *>(dst + (int64_t)kt * KT_BYTES)[16 + p] = lo;
-        if constexpr (MDec<DT>::OFF) {
-            // block b's four pieces: 4b .. 4b+3 (Q4_1) or, for the K formats,
-            // 8 (b >> 1) + 4 (b & 1) .. + 3: four neighbouring lanes either way
-            sum += __shfl_xor(sum, 1, 64);
-            sum += __shfl_xor(sum, 2, 64);
-            const float s0 = __shfl(sum, (t & 48) + 0, 64), s1 = __shfl(sum, (t & 48) + 4, 64);
-            const float s2 = __shfl(sum, (t & 48) + 8, 64), s3 = __shfl(sum, (t & 48) + 12, 64);
-            if (p == 0) {
-                const float s[4] = {s0, s2, s1, s3};
-                half8 o;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    o[j] = (_Float16)s[j];
-                    const float r = s[j] - (float)o[j];
-                    o[4 + j] = (_Float16)(r == r ? r : 0.f);
-                }
-                ws.sums[row * nkt + kt] = __builtin_bit_cast(uint4, o);
-            }
+        for (int j = 0; j < PPL; j++)
+            if (lane + 64 * j < n) put_piece<DT>(ws, row, nkt, lane + 64 * j, va[j], vb[j], mul);
+    } else {
+        for (int i = lane; i < n; i += 64) {
+            load(i, va[0], vb[0]);
+            put_piece<DT>(ws, row, nkt, i, va[0], vb[0], mul);
         }
     }
 }
@@ -420,27 +506,37 @@ struct MoeGemmArgs {
 };
 
 // A workgroup: W wavefronts, each 2 x 32 rows (swiglu: 32 gate rows and the
-// same 32 up rows) against the BN = 32 FN slots of a tile.
+// same 32 up rows) against the BN = 32 FN slots of a tile.  Weights: a
+// wavefront loads its own rows' bytes of a k-tile in runs of 64 or 128 bytes
+// (lanes reading a row each would touch 32 cache lines per instruction), parks
+// them in its part of LDS one k-tile ahead and reads each lane's bytes from
+// there.  Activations: all wavefronts share the tile's rows, double-buffered.
 template <int DT, int FN, int W, bool SWI>
 __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a) {
     using D = MDec<DT>;
     constexpr int BN = 32 * FN, RW = SWI ? 32 : 64, BM = RW * W;
-    constexpr int NP = BN * 32 / (64 * W);  // 16-byte pieces of a k-tile per thread
+    constexpr int NP = BN * 16 / (64 * W);  // 16-byte pieces of half a k-tile per thread
     static_assert(NP >= 1, "tile too small for the workgroup");
-    __shared__ __attribute__((aligned(16))) uint8_t xl[2][BN * KT_BYTES];
+    constexpr int RI = 64 / D::LP, MI = 64 / RI;  // rows per main load instruction, instructions per k-tile
+    __shared__ __attribute__((aligned(16))) uint8_t xl[2][BN * XT_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t wl[W][64 * D::ROW];
     __shared__ int32_t slot_of[BN];
     __shared__ float rsc[BN];
     const int t = (int)threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l32 = lane & 31, kh = lane >> 5;
 
-    // workgroups of one XCD (id mod 8) take neighbouring tiles of slots for
-    // the same rows of the matrix: the slots of an expert meet in one L2
+    // An XCD (workgroup id mod 8) takes a run of jobs, ordered by expert, then
+    // rows of its matrix, then its tiles of slots: the workgroups running on it
+    // at a time share one expert's slots (a few MB, its L2) and read the same
+    // rows together
     const int nt = a.ws.tiles[0].x, total = nt * a.mtiles, chunk = (total + 7) / 8;
     const int id = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
     if (((int)blockIdx.x >> 3) >= chunk || id >= total) return;
-    const int mt = id / nt;
-    const int4 tile = a.ws.tiles[1 + id % nt];
-    const int e = __builtin_amdgcn_readfirstlane(tile.x), n_rows = __builtin_amdgcn_readfirstlane(tile.z);
+    const int4 of_job = a.ws.tiles[1 + id / a.mtiles];  // some tile of the job's expert
+    const int t0 = of_job.w, tc = of_job.z >> 8, r_id = id - t0 * a.mtiles;
+    const int mt = r_id / tc;
+    const int4 tile = a.ws.tiles[1 + t0 + r_id % tc];
+    const int e = __builtin_amdgcn_readfirstlane(tile.x), n_rows = __builtin_amdgcn_readfirstlane(tile.z & 0xFF);
     for (int i = t; i < BN; i += 64 * W) {
         const int s = i < n_rows ? a.ws.order[tile.y + i] : -1;
         slot_of[i] = s;
@@ -448,16 +544,18 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
     }
     __syncthreads();
 
-    // activation pieces: piece c of thread t is 16-byte piece t % 32 of row t / 32 + c (2 W)
+    // activation pieces: piece c of thread t is 16-byte piece t % 16 of row t / 16 + c (4 W),
+    // kept at piece (t % 16) ^ (row % 16) in LDS: 16 rows' reads of one piece
+    // fall on 16 different bank groups
     uint32_t xoff[NP];
     uint32_t xdst[NP];
 #pragma unroll
     for (int c = 0; c < NP; c++) {
-        const int r = (t >> 5) + c * (2 * W), p = t & 31;
+        const int r = (t >> 4) + c * (4 * W), p = t & 15;
         const int s = slot_of[r];
         // rows past the tile's end read nothing (zeros)
         xoff[c] = s >= 0 ? (uint32_t)(s / a.T) * (uint32_t)(a.nkt * KT_BYTES) + 16u * p : 0xFFFFFFF0u - (uint32_t)(a.nkt * KT_BYTES);
-        xdst[c] = (uint32_t)(r * KT_BYTES + 16 * ((p & 16) | ((p ^ r) & 15)));
+        xdst[c] = (uint32_t)(r * XT_BYTES + 16 * ((p ^ r) & 15));
     }
     const Rsrc xrs = make_rsrc_uniform(a.ws.xs, a.xs_bytes);
 
@@ -469,8 +567,12 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
     const uint32_t nb0 = left > 0 ? (uint32_t)((left < RW ? left : RW) * a.row_bytes) + mis : 0u;
     const Rsrc wr0 = make_rsrc_uniform(a.w0 + (base - mis), nb0);
     const Rsrc wr1 = SWI ? make_rsrc_uniform(a.w1 + (base - mis), nb0) : wr0;
-    const uint32_t ro0 = mis + (uint32_t)l32 * (uint32_t)a.row_bytes;
-    const uint32_t ro1 = SWI ? ro0 : ro0 + 32u * (uint32_t)a.row_bytes;
+    const uint32_t rb = (uint32_t)a.row_bytes;
+    const uint32_t so1 = SWI ? 0u : 32u * rb;   // the second 32 rows: of the up matrix, or further down
+    const uint32_t moff = mis + (uint32_t)(lane / D::LP) * rb + 16u * (uint32_t)(lane % D::LP);
+    const uint32_t eoff = mis + (uint32_t)l32 * rb;
+    uint8_t *const wmain = &wl[wave][(lane / D::LP) * D::ROW + 16 * (lane % D::LP)];
+    uint8_t *const wrow[2] = {&wl[wave][l32 * D::ROW], &wl[wave][(32 + l32) * D::ROW]};
 
     // block sums of the lane's slots (formats with minima): lane half 0 alone
     const uint4 *sump[FN];
@@ -490,75 +592,119 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
 #pragma unroll
             for (int j = 0; j < 16; j++) acc[i][f][j] = 0.f;
 
-    uint32_t raw[2][D::NW];
-    u32x4_t xr[(NP + 1) / 2];
-    auto fetch_w = [&](int kt, int g) {
-        D::load(wr0, ro0, kt, kh, g, raw[0]);
-        D::load(wr1, ro1, kt, kh, g, raw[1]);
-    };
-    // the activations of a k-tile move in two halves through registers
-    auto fetch_x = [&](int kt, int h) {
+    u32x4_t wm[MI];
+    typename D::Extra wx[2];
+    auto fetch_w = [&](int kt) {
+        const uint32_t tb = D::TB(kt);
 #pragma unroll
-        for (int c = 0; c < NP; c++)
-            if (c * 2 / NP == h) xr[c % ((NP + 1) / 2)] = __builtin_amdgcn_raw_buffer_load_b128(xrs, xoff[c], (uint32_t)(kt * KT_BYTES), 0);
+        for (int i = 0; i < MI; i++) {
+            const int h = i / (MI / 2), r = (i % (MI / 2)) * RI;
+            wm[i] = ld128(h ? wr1 : wr0, moff, tb + (h ? so1 : 0u) + (uint32_t)r * rb);
+        }
+        D::load(wr0, eoff, kt, kh, wx[0]);
+        D::load(wr1, eoff + so1, kt, kh, wx[1]);
     };
-    auto store_x = [&](int buf, int h) {
-#pragma unroll
-        for (int c = 0; c < NP; c++)
-            if (c * 2 / NP == h) *reinterpret_cast<u32x4_t *>(&xl[buf][xdst[c]]) = xr[c % ((NP + 1) / 2)];
-    };
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        fetch_x(0, h);
-        store_x(0, h);
+    // A row of 18- or 34-byte blocks may end inside a dword, which reads as 0
+    // where it reaches past the matrix: its last two bytes are loaded by
+    // themselves, once, and written over the last k-tile's (into the padding of
+    // the others').
+    constexpr bool TAIL = DT == QMM_Q4_0 || DT == QMM_Q8_0;
+    uint32_t tail[2] = {0u, 0u};
+    if constexpr (TAIL) {
+        tail[0] = ld16(wr0, eoff + rb - 2u, 0u);
+        tail[1] = ld16(wr1, eoff + so1 + rb - 2u, 0u);
     }
+    auto store_w = [&](int kt) {
 #pragma unroll
-    for (int g = 0; g < D::NG; g++) fetch_w(0, g);
+        for (int i = 0; i < MI; i++) *reinterpret_cast<u32x4_t *>(wmain + i * RI * D::ROW) = wm[i];
+        D::store(wrow[0], kh, wx[0]);
+        D::store(wrow[1], kh, wx[1]);
+        if constexpr (TAIL) {
+            const int at = kt == a.nkt - 1 ? (int)rb - (int)D::TB(kt) - 2 : D::ROW - 4;
+            *reinterpret_cast<uint16_t *>(wrow[0] + at) = (uint16_t)tail[0];
+            *reinterpret_cast<uint16_t *>(wrow[1] + at) = (uint16_t)tail[1];
+        }
+    };
+    uint32_t raw[2][D::NW];
+    auto read_w = [&](int g) {
+        D::read(wrow[0], kh, g, raw[0]);
+        D::read(wrow[1], kh, g, raw[1]);
+    };
+    u32x4_t xr[NP];
+    const int nx = 2 * a.nkt;  // half k-tiles
+    auto fetch_x = [&](int x) {  // past the last one: the last again, unused
+#pragma unroll
+        for (int c = 0; c < NP; c++) xr[c] = ld128(xrs, xoff[c], (uint32_t)((x < nx ? x : nx - 1) * XT_BYTES));
+    };
+    auto store_x = [&](int buf) {
+#pragma unroll
+        for (int c = 0; c < NP; c++) *reinterpret_cast<u32x4_t *>(&xl[buf][xdst[c]]) = xr[c];
+    };
+    fetch_x(0);
+    fetch_w(0);
+    store_x(0);
+    fetch_x(1);
+    store_w(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    read_w(0);
     __syncthreads();
 
     for (int kt = 0; kt < a.nkt; kt++) {
-        const int buf = kt & 1;
-        // the next k-tile's loads (past the last one: the last again, unused)
-        const int kn = kt + 1 < a.nkt ? kt + 1 : kt;
-        fetch_x(kn, 0);
-        half8 so_a[FN];
-        if constexpr (D::OFF) {
-#pragma unroll
-            for (int f = 0; f < FN; f++) {
-                const uint4 v = sump[f][kt];
-                so_a[f] = kh == 0 ? __builtin_bit_cast(half8, v) : half8{0, 0, 0, 0, 0, 0, 0, 0};
-            }
-        }
+        const int kn = kt + 1 < a.nkt ? kt + 1 : kt;  // past the last k-tile: the last again, unused
+        uint4 so_a[FN];
         const int nb = (a.K - kt * KT) / 32;
         typename D::Pre pre[2];
-#pragma unroll
-        for (int i = 0; i < 2; i++) D::prep(raw[i], kt, nb, pre[i]);
-        const uint8_t *xb = &xl[buf][l32 * KT_BYTES];
         floatx16 tmp[2][FN];
 #pragma unroll
         for (int n = 0; n < 8; n++) {
-            const int st = D::step(n);
+            const int st = D::step(n), h = n >> 2;
+            if (n % 4 == 0) {
+                // half h of the k-tile: the other buffer takes the half after it
+                // (fetched half a k-tile ago), and the one after that sets out
+                store_x(h ^ 1);
+                fetch_x(2 * kt + h + 2);
+            }
+            if (n == 0) {
+                fetch_w(kn);
+#pragma unroll
+                for (int i = 0; i < 2; i++) D::prep(raw[i], kt, nb, pre[i]);
+            }
+            if constexpr (D::OFF) {
+                // block sums for the step at the k-tile's (super-block's) end
+                if (n == 4 && (!D::PAIR || (kt & 1))) {
+#pragma unroll
+                    for (int f = 0; f < FN; f++) so_a[f] = sump[f][D::PAIR ? kt - 1 + kh : kt];
+                }
+            }
+            if (n % (8 / D::NG) == 0 && n / (8 / D::NG) + 1 < D::NG) read_w(n / (8 / D::NG) + 1);
             half8 b[2];
 #pragma unroll
             for (int i = 0; i < 2; i++) b[i] = D::frag(raw[i], st, kt, pre[i]);
-            const int p = ((2 * st + kh) ^ l32) & 15;
+            const uint8_t *xb = &xl[h][l32 * XT_BYTES];
+            const int p = ((2 * (n & 3) + kh) ^ l32) & 15;
+            half8 ah[FN], al[FN];
 #pragma unroll
             for (int f = 0; f < FN; f++) {
-                const half8 ah = *reinterpret_cast<const half8 *>(xb + 32 * f * KT_BYTES + 16 * p);
-                const half8 al = *reinterpret_cast<const half8 *>(xb + 32 * f * KT_BYTES + 256 + 16 * p);
+                ah[f] = *reinterpret_cast<const half8 *>(xb + 32 * f * XT_BYTES + 16 * p);
+                al[f] = *reinterpret_cast<const half8 *>(xb + 32 * f * XT_BYTES + 16 * (p ^ 8));
+            }
+#pragma unroll
+            for (int f = 0; f < FN; f++)
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     if (n % D::STEPS == 0) {
                         floatx16 z;
 #pragma unroll
                         for (int j = 0; j < 16; j++) z[j] = 0.f;
-                        tmp[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, b[i], z, 0, 0, 0);
+                        tmp[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[f], b[i], z, 0, 0, 0);
                     } else {
-                        tmp[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, b[i], tmp[i][f], 0, 0, 0);
+                        tmp[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[f], b[i], tmp[i][f], 0, 0, 0);
                     }
-                    tmp[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, b[i], tmp[i][f], 0, 0, 0);
                 }
-            }
+#pragma unroll
+            for (int f = 0; f < FN; f++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) tmp[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[f], b[i], tmp[i][f], 0, 0, 0);
             if ((n + 1) % D::STEPS == 0) {
                 // the end of a chain: scale its sum once, in f32
 #pragma unroll
@@ -570,32 +716,50 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
                         for (int j = 0; j < 16; j++) acc[i][f][j] = fmaf(s, tmp[i][f][j], acc[i][f][j]);
                 }
             }
-            if ((n + 1) % (8 / D::NG) == 0) fetch_w(kn, n / (8 / D::NG));
-            if (n == 3) {
-                store_x(buf ^ 1, 0);
-                fetch_x(kn, 1);
-            }
+            if (n == 3) __syncthreads();
             // one chain's sums at a time: left alone the compiler starts
             // several and spills them
-            if ((n + 1) % D::STEPS == 0 || n == 3) __builtin_amdgcn_sched_barrier(0);
+            else if ((n + 1) % D::STEPS == 0) __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (D::OFF) {
+            if (!D::PAIR || (kt & 1)) {
+                float so[2];
+                half8 off[2], sa[FN];
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                float so;
-                const half8 off = D::offset(pre[i], so);
+                for (int f = 0; f < FN; f++)
+                    sa[f] = D::PAIR || kh == 0 ? __builtin_bit_cast(half8, so_a[f]) : half8{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                for (int f = 0; f < FN; f++) {
-                    floatx16 z;
+                for (int i = 0; i < 2; i++) off[i] = D::offset(raw[i], kh, pre[i], so[i]);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) z[j] = 0.f;
-                    z = __builtin_amdgcn_mfma_f32_32x32x16_f16(so_a[f], off, z, 0, 0, 0);
+                for (int f = 0; f < FN; f++)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) acc[i][f][j] = fmaf(so, z[j], acc[i][f][j]);
+                    for (int i = 0; i < 2; i++) {
+                        if constexpr (D::PAIR) {
+                            floatx16 z;
+#pragma unroll
+                            for (int j = 0; j < 16; j++) z[j] = 0.f;
+                            tmp[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(sa[f], off[i], z, 0, 0, 0);
+                        } else {
+                            acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(sa[f], off[i], acc[i][f], 0, 0, 0);
+                        }
+                    }
+                if constexpr (D::PAIR) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int f = 0; f < FN; f++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+#pragma unroll
+                            for (int j = 0; j < 16; j++) acc[i][f][j] = fmaf(so[i], tmp[i][f][j], acc[i][f][j]);
                 }
             }
         }
-        store_x(buf ^ 1, 1);
+        // this wavefront has read all of its raw bytes: the next k-tile's take
+        // their place, and no other wavefront sees them
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        store_w(kn);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        read_w(0);
         __syncthreads();
     }
 
@@ -618,25 +782,47 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
         }
 }
 
-// out[slot][:] = 0 where a slot has no expert (the GEMM writes no such row)
-__global__ void __launch_bounds__(256) moe_zero_kernel(const int32_t *ids, int E, int64_t M, float *out) {
-    const int64_t s = blockIdx.x;
-    const int e = ids[s];
-    if (e >= 0 && e < E) return;
-    for (int64_t m = threadIdx.x; m < M; m += 256) out[s * M + m] = 0.f;
-}
-
-// Y[n][m] = residual[n][m] + sum over t of weights[n][t] * prod[n T + t][m]
+// Y[n][m] = residual[n][m] + sum over t of weights[n][t] * prod[n T + t][m], t
+// ascending.  V values per thread (4: M % 4 == 0 and 16-byte aligned rows).
+// Four slots' rows are in flight at once; a slot without an expert is an empty
+// resource (zeros) under weight 0.
+template <int V>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const int32_t *ids, const float *weights, const float *prod,
                                                           const float *residual, float *Y, int E, int64_t M, int T) {
     const int64_t n = blockIdx.x;
-    for (int64_t m = (int64_t)blockIdx.y * 256 + threadIdx.x; m < M; m += (int64_t)gridDim.y * 256) {
-        float y = residual ? residual[n * M + m] : 0.f;
-        for (int t = 0; t < T; t++) {
-            const int e = ids[n * T + t];
-            if (e >= 0 && e < E) y = fmaf(weights[n * T + t], prod[(n * T + t) * M + m], y);
+    const uint32_t bytes = 4u * (uint32_t)M;
+    const Rsrc rr = make_rsrc_uniform(residual ? residual + n * M : prod, residual ? bytes : 0u);
+    const Rsrc ry = make_rsrc_uniform(Y + n * M, bytes);
+    for (uint32_t off = 4u * V * (blockIdx.y * 256u + threadIdx.x); off < bytes; off += 4u * V * 256u * gridDim.y) {
+        float y[V];
+        auto get = [&](Rsrc rs, float (&v)[V]) {
+            if constexpr (V == 4) {
+                const floatx4 q = __builtin_bit_cast(floatx4, ld128(rs, off, 0));
+                v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+            } else {
+                v[0] = __builtin_bit_cast(float, ld32(rs, off, 0));
+            }
+        };
+        get(rr, y);
+        for (int t0 = 0; t0 < T; t0 += 4) {
+            float v[4][V], w[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int64_t s = n * T + (t0 + j < T ? t0 + j : T - 1);
+                const int e = ids[s];
+                const bool live = t0 + j < T && e >= 0 && e < E;
+                w[j] = live ? weights[s] : 0.f;
+                get(make_rsrc_uniform(prod + s * M, live ? bytes : 0u), v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int i = 0; i < V; i++) y[i] = fmaf(w[j], v[j][i], y[i]);
         }
-        Y[n * M + m] = y;
+        if constexpr (V == 4)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, floatx4{y[0], y[1], y[2], y[3]}), ry, off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y[0]), ry, off, 0, 0);
     }
 }
 
@@ -684,7 +870,10 @@ void launch_gemm(const MoeGemmArgs &a, int64_t tiles, hipStream_t st) {
 template <int DT, bool SWI>
 hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, const int32_t *ids,
                     const float *weights, const float *X, const float *residual, float *out, void *work, hipStream_t st) {
-    constexpr int W = 4;
+#ifndef MOE_W
+#define MOE_W 4
+#endif
+    constexpr int W = MOE_W;
     const int BN = moe_gemm_bn(E, N, T);
     const MoeSizes z = moe_sizes(DT, E, M, K, N, T, BN, !SWI);
     uint8_t *p = static_cast<uint8_t *>(work);
@@ -705,16 +894,25 @@ hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_
         const int32_t *idc = ids + n0 * T;
         a.xs_bytes = (uint32_t)(rows * z.nkt * KT_BYTES);
         a.out = SWI ? out + n0 * T * M : a.ws.prod;
-        hipLaunchKernelGGL((moe_prep_kernel<DT>), dim3((unsigned)(rows + 1)), dim3(256), 0, st, idc, (int)S, (int)E, BN, a.ws, X + n0 * (SWI ? 1 : T) * K, rows, (int)K, (int)z.nkt, SWI ? 0 : 1);
+        const dim3 pg((unsigned)((rows + 7) / 8 + 1));
+        const float *xc = X + n0 * (SWI ? 1 : T) * K;
+        if (K <= 4096)
+            hipLaunchKernelGGL((moe_prep_kernel<DT, true>), pg, dim3(512), 0, st, idc, (int)S, (int)E, BN, a.ws, xc, rows, (int)K,
+                               (int)z.nkt, (int)T, !SWI, a.out, M);
+        else
+            hipLaunchKernelGGL((moe_prep_kernel<DT, false>), pg, dim3(512), 0, st, idc, (int)S, (int)E, BN, a.ws, xc, rows, (int)K,
+                               (int)z.nkt, (int)T, !SWI, a.out, M);
         const int64_t tiles = S / BN + std::min(E, S);
         if (BN == 32) launch_gemm<DT, 1, W, SWI>(a, tiles, st);
         else launch_gemm<DT, 2, W, SWI>(a, tiles, st);
-        if (SWI) {
-            hipLaunchKernelGGL(moe_zero_kernel, dim3((unsigned)S), dim3(256), 0, st, idc, (int)E, M, a.out);
-        } else {
-            const unsigned gy = (unsigned)std::min<int64_t>((M + 255) / 256, 64);
-            hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)n, gy), dim3(256), 0, st, idc, weights + n0 * T, a.ws.prod,
-                               residual ? residual + n0 * M : nullptr, out + n0 * M, (int)E, M, (int)T);
+        if (!SWI) {
+            const float *res = residual ? residual + n0 * M : nullptr;
+            float *y = out + n0 * M;
+            const bool vec = M % 4 == 0 && ((uintptr_t)res & 15) == 0 && ((uintptr_t)y & 15) == 0;
+            const int64_t per = vec ? 1024 : 256;
+            const dim3 cg((unsigned)n, (unsigned)std::min<int64_t>((M + per - 1) / per, 64));
+            if (vec) hipLaunchKernelGGL((moe_combine_kernel<4>), cg, dim3(256), 0, st, idc, weights + n0 * T, a.ws.prod, res, y, (int)E, M, (int)T);
+            else hipLaunchKernelGGL((moe_combine_kernel<1>), cg, dim3(256), 0, st, idc, weights + n0 * T, a.ws.prod, res, y, (int)E, M, (int)T);
         }
     }
     return hipGetLastError();
