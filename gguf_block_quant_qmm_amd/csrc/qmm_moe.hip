@@ -264,25 +264,40 @@ hipError_t run_gemv(const void *w0, const void *w1, int64_t E, int64_t M, int64_
     return hipGetLastError();
 }
 
-// Few tokens run the GEMV form.  A tuning lever of measurement builds only.
-bool use_gemm(int64_t N) {
-    static const int lever = tuning_lever("QMM_MOE_GEMM_FROM_N", 8);
-    return N >= lever;
+// Which form: the few-token kernel reads an expert's bytes for every slot (4 to 5
+// TB/s), the matrix cores once per touched expert (2 to 2.5 TB/s while memory
+// bounds them) after two more launches (about 20 us).  With S slots over E
+// experts the two meet at S = 2 E, where an expert that is touched has 2.3
+// slots: 64 experts, 8 of them each, gate/up 1024 x 2048 Q4_K, 16 tokens: 57
+// against 60 us (8: 33 against 54, 24: 88 against 61); 8 experts, 2 each, 14336 x
+// 4096: 8 tokens 198 against 190 us (4: 108 against 138, 16: 365 against 205).
+// Below 80 MB of reads in all the few-token kernel is done before the other
+// form's launches are.  A measurement build takes QMM_MOE_GEMM_FROM_N = n to
+// decide by the tokens alone.
+bool use_gemm(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, bool down) {
+    static const int lever = tuning_lever("QMM_MOE_GEMM_FROM_N", 0);
+    if (lever) return N >= lever;
+    const int64_t S = N * T;
+    if (S > (int64_t(1) << 30) / M) return true;  // the few-token grid's limit
+    const int bs = dtype == QMM_Q4_K || dtype == QMM_Q5_K || dtype == QMM_Q6_K ? 256 : 32;
+    const int bb = dtype == QMM_Q4_0 ? 18 : dtype == QMM_Q4_1 ? 20 : dtype == QMM_Q8_0 ? 34 : dtype == QMM_Q4_K ? 144 : dtype == QMM_Q5_K ? 176 : 210;
+    const int64_t row = K / bs * bb, expert = (down ? 1 : 2) * M * row;
+    return S >= 2 * E && expert >= (int64_t(80) << 20) / S;
 }
 
 }  // namespace
 
 int64_t moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
-    return use_gemm(N) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, false) : 0;
+    return use_gemm(dtype, E, M, K, N, T, false) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, false) : 0;
 }
 int64_t moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T) {
-    return use_gemm(N) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, true) : 0;
+    return use_gemm(dtype, E, M, K, N, T, true) ? moe_gemm_work_bytes(dtype, E, M, K, N, T, true) : 0;
 }
 
 hipError_t launch_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N,
                              int64_t T, const int32_t *ids, const float *X, float *out, void *work, hipStream_t st,
                              int cus) {
-    if (use_gemm(N)) return launch_moe_gemm_swiglu(gate, up, dtype, E, M, K, N, T, ids, X, out, work, st);
+    if (use_gemm(dtype, E, M, K, N, T, false)) return launch_moe_gemm_swiglu(gate, up, dtype, E, M, K, N, T, ids, X, out, work, st);
 #define QMM_CALL(DT) return run_gemv<DT, true>(gate, up, E, M, K, N, T, ids, nullptr, X, nullptr, out, st, cus)
     QMM_MOE_DT(dtype, QMM_CALL)
 #undef QMM_CALL
@@ -292,7 +307,7 @@ hipError_t launch_moe_swiglu(const void *gate, const void *up, int dtype, int64_
 hipError_t launch_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T,
                            const int32_t *ids, const float *weights, const float *H, const float *residual, float *Y,
                            void *work, hipStream_t st, int cus) {
-    if (use_gemm(N)) return launch_moe_gemm_down(w, dtype, E, M, K, N, T, ids, weights, H, residual, Y, work, st);
+    if (use_gemm(dtype, E, M, K, N, T, true)) return launch_moe_gemm_down(w, dtype, E, M, K, N, T, ids, weights, H, residual, Y, work, st);
 #define QMM_CALL(DT) return run_gemv<DT, false>(w, nullptr, E, M, K, N, T, ids, weights, H, residual, Y, st, cus)
     QMM_MOE_DT(dtype, QMM_CALL)
 #undef QMM_CALL

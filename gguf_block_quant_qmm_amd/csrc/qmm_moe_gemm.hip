@@ -332,7 +332,7 @@ struct MoeWs {
     float *rscale;    // per row: what the split row was divided by
     uint4 *sums;      // [row][k-tile]: 4 block sums, hi and lo (formats with minima)
     uint8_t *xs;      // [row][half k-tile][hi, lo][8 pieces of 8 values]
-    float *prod;      // down: [slot][M]
+    float *prod;      // down: [split][slot][M]; gate/up with splits: [split][slot][gate, up][M]
 };
 
 // Block 0 sorts the S slots by expert and cuts each expert's run into tiles of
@@ -502,6 +502,8 @@ struct MoeGemmArgs {
     float *out;              // swiglu: out[slot][M]; down: prod[slot][M]
     int64_t M, row_bytes, mat_bytes;
     int K, nkt, mtiles, T;   // T: slots per activation row (1 when every slot has its own)
+    int splits, kper;        // workgroups that share a row tile's K, k-tiles of each (even)
+    int64_t part_stride;     // floats between the splits' parts in ws.prod
     uint32_t xs_bytes;       // of ws.xs
 };
 
@@ -529,12 +531,14 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
     // rows of its matrix, then its tiles of slots: the workgroups running on it
     // at a time share one expert's slots (a few MB, its L2) and read the same
     // rows together
-    const int nt = a.ws.tiles[0].x, total = nt * a.mtiles, chunk = (total + 7) / 8;
+    const int per_tile = a.mtiles * a.splits;
+    const int nt = a.ws.tiles[0].x, total = nt * per_tile, chunk = (total + 7) / 8;
     const int id = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
     if (((int)blockIdx.x >> 3) >= chunk || id >= total) return;
-    const int4 of_job = a.ws.tiles[1 + id / a.mtiles];  // some tile of the job's expert
-    const int t0 = of_job.w, tc = of_job.z >> 8, r_id = id - t0 * a.mtiles;
-    const int mt = r_id / tc;
+    const int4 of_job = a.ws.tiles[1 + id / per_tile];  // some tile of the job's expert
+    const int t0 = of_job.w, tc = of_job.z >> 8, r_id = id - t0 * per_tile;
+    const int mt = r_id / tc / a.splits, split = r_id / tc % a.splits;
+    const int k0 = split * a.kper, k1 = k0 + a.kper < a.nkt ? k0 + a.kper : a.nkt;  // k-tiles [k0, k1)
     const int4 tile = a.ws.tiles[1 + t0 + r_id % tc];
     const int e = __builtin_amdgcn_readfirstlane(tile.x), n_rows = __builtin_amdgcn_readfirstlane(tile.z & 0xFF);
     for (int i = t; i < BN; i += 64 * W) {
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
         D::read(wrow[1], kh, g, raw[1]);
     };
     u32x4_t xr[NP];
-    const int nx = 2 * a.nkt;  // half k-tiles
+    const int nx = 2 * k1;  // past the last half k-tile
     auto fetch_x = [&](int x) {  // past the last one: the last again, unused
 #pragma unroll
         for (int c = 0; c < NP; c++) xr[c] = ld128(xrs, xoff[c], (uint32_t)((x < nx ? x : nx - 1) * XT_BYTES));
@@ -640,17 +644,17 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
 #pragma unroll
         for (int c = 0; c < NP; c++) *reinterpret_cast<u32x4_t *>(&xl[buf][xdst[c]]) = xr[c];
     };
-    fetch_x(0);
-    fetch_w(0);
+    fetch_x(2 * k0);
+    fetch_w(k0);
     store_x(0);
-    fetch_x(1);
-    store_w(0);
+    fetch_x(2 * k0 + 1);
+    store_w(k0);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     read_w(0);
     __syncthreads();
 
-    for (int kt = 0; kt < a.nkt; kt++) {
-        const int kn = kt + 1 < a.nkt ? kt + 1 : kt;  // past the last k-tile: the last again, unused
+    for (int kt = k0; kt < k1; kt++) {
+        const int kn = kt + 1 < k1 ? kt + 1 : kt;  // past the last k-tile: the last again, unused
         uint4 so_a[FN];
         const int nb = (a.K - kt * KT) / 32;
         typename D::Pre pre[2];
@@ -772,23 +776,29 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
             const int64_t s = slot_of[r];
             const float sc = rsc[r];
             if (s >= 0) {
-                if constexpr (SWI) {
-                    if (l32 < left) a.out[s * a.M + m0 + l32] = silu(acc[0][f][j] * sc) * (acc[1][f][j] * sc);
+                const float v0 = acc[0][f][j] * sc, v1 = acc[1][f][j] * sc;
+                if (SWI && a.splits == 1) {
+                    if (l32 < left) a.out[s * a.M + m0 + l32] = silu(v0) * v1;
+                } else if (SWI) {
+                    float *o = a.ws.prod + split * a.part_stride + 2 * s * a.M + m0 + l32;
+                    if (l32 < left) { o[0] = v0; o[a.M] = v1; }
                 } else {
-                    if (l32 < left) a.out[s * a.M + m0 + l32] = acc[0][f][j] * sc;
-                    if (l32 + 32 < left) a.out[s * a.M + m0 + 32 + l32] = acc[1][f][j] * sc;
+                    float *o = a.ws.prod + split * a.part_stride + s * a.M + m0 + l32;
+                    if (l32 < left) o[0] = v0;
+                    if (l32 + 32 < left) o[32] = v1;
                 }
             }
         }
 }
 
 // Y[n][m] = residual[n][m] + sum over t of weights[n][t] * prod[n T + t][m], t
-// ascending.  V values per thread (4: M % 4 == 0 and 16-byte aligned rows).
+// ascending, a slot's product the sum of its splits' parts.  V values per thread (4: M % 4 == 0 and 16-byte aligned rows).
 // Four slots' rows are in flight at once; a slot without an expert is an empty
 // resource (zeros) under weight 0.
 template <int V>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const int32_t *ids, const float *weights, const float *prod,
-                                                          const float *residual, float *Y, int E, int64_t M, int T) {
+                                                          const float *residual, float *Y, int E, int64_t M, int T,
+                                                          int splits, int64_t part_stride) {
     const int64_t n = blockIdx.x;
     const uint32_t bytes = 4u * (uint32_t)M;
     const Rsrc rr = make_rsrc_uniform(residual ? residual + n * M : prod, residual ? bytes : 0u);
@@ -813,6 +823,12 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const int32_t *ids, co
                 const bool live = t0 + j < T && e >= 0 && e < E;
                 w[j] = live ? weights[s] : 0.f;
                 get(make_rsrc_uniform(prod + s * M, live ? bytes : 0u), v[j]);
+                for (int p = 1; p < splits; p++) {
+                    float u[V];
+                    get(make_rsrc_uniform(prod + p * part_stride + s * M, live ? bytes : 0u), u);
+#pragma unroll
+                    for (int i = 0; i < V; i++) v[j][i] += u[i];
+                }
             }
 #pragma unroll
             for (int j = 0; j < 4; j++)
@@ -823,6 +839,22 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const int32_t *ids, co
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, floatx4{y[0], y[1], y[2], y[3]}), ry, off, 0, 0);
         else
             __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y[0]), ry, off, 0, 0);
+    }
+}
+
+// out[slot][m] = silu(sum of the splits' gate parts) * (sum of their up parts)
+__global__ void __launch_bounds__(256) moe_silu_parts_kernel(const int32_t *ids, const float *prod, float *out, int E, int64_t M,
+                                                             int splits, int64_t part_stride) {
+    const int64_t s = blockIdx.x;
+    const int e = ids[s];
+    if (e < 0 || e >= E) return;  // already cleared
+    for (int64_t m = (int64_t)blockIdx.y * 256 + threadIdx.x; m < M; m += (int64_t)gridDim.y * 256) {
+        float g = 0.f, u = 0.f;
+        for (int p = 0; p < splits; p++) {
+            g += prod[p * part_stride + 2 * s * M + m];
+            u += prod[p * part_stride + (2 * s + 1) * M + m];
+        }
+        out[s * M + m] = silu(g) * u;
     }
 }
 
@@ -840,8 +872,10 @@ int64_t chunk_tokens(int64_t K, int64_t M, int64_t N, int64_t T, bool down) {
     return std::max<int64_t>(1, std::min(n, N));
 }
 
+constexpr int GEMM_W = 4;  // wavefronts per workgroup
+
 struct MoeSizes {
-    int64_t tokens, slots, rows, nkt, tiles;
+    int64_t tokens, slots, rows, nkt, tiles, mtiles, splits, kper;
     int64_t o_order, o_rscale, o_sums, o_xs, o_prod, bytes;
 };
 MoeSizes moe_sizes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, int BN, bool down) {
@@ -851,29 +885,35 @@ MoeSizes moe_sizes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_
     z.rows = down ? z.slots : z.tokens;
     z.nkt = (K + KT - 1) / KT;
     z.tiles = z.slots / BN + std::min(E, z.slots);
+    z.mtiles = (M + (down ? 64 : 32) * GEMM_W - 1) / ((down ? 64 : 32) * GEMM_W);
+    // Few jobs (a workgroup alone on its CU needs ~2 us per k-tile): the k-tiles
+    // of a row tile are shared out, at least 8 each, until two workgroups per CU
+    // have one.  Two wide experts' down projection, 30 tokens, 8 x 4096 x 14336
+    // Q4_K: 253 us in one piece.
+    const int64_t jobs = std::max<int64_t>(1, std::min(z.tiles, std::min(E, z.slots) + z.slots / (2 * BN)) * z.mtiles);
+    z.splits = std::max<int64_t>(1, std::min<int64_t>({512 / jobs, z.nkt / 8, 8}));
+    z.kper = ((z.nkt + z.splits - 1) / z.splits + 1) / 2 * 2;
+    z.splits = (z.nkt + z.kper - 1) / z.kper;
     const bool off = dtype == QMM_Q4_1 || dtype == QMM_Q4_K || dtype == QMM_Q5_K;
     z.o_order = align256(16 * (1 + z.tiles));
     z.o_rscale = z.o_order + align256(4 * z.slots);
     z.o_sums = z.o_rscale + align256(4 * z.rows);
     z.o_xs = z.o_sums + (off ? align256(16 * z.rows * z.nkt) : 0);
     z.o_prod = z.o_xs + align256(z.rows * z.nkt * KT_BYTES);
-    z.bytes = z.o_prod + (down ? align256(4 * z.slots * M) : 0);
+    z.bytes = z.o_prod + (down ? align256(4 * z.splits * z.slots * M) : z.splits > 1 ? align256(8 * z.splits * z.slots * M) : 0);
     return z;
 }
 
 template <int DT, int FN, int W, bool SWI>
 void launch_gemm(const MoeGemmArgs &a, int64_t tiles, hipStream_t st) {
-    const int64_t blocks = (tiles * a.mtiles + 7) / 8 * 8;
+    const int64_t blocks = (tiles * a.mtiles * a.splits + 7) / 8 * 8;
     hipLaunchKernelGGL((moe_gemm_kernel<DT, FN, W, SWI>), dim3((unsigned)blocks), dim3(64 * W), 0, st, a);
 }
 
 template <int DT, bool SWI>
 hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, const int32_t *ids,
                     const float *weights, const float *X, const float *residual, float *out, void *work, hipStream_t st) {
-#ifndef MOE_W
-#define MOE_W 4
-#endif
-    constexpr int W = MOE_W;
+    constexpr int W = GEMM_W;
     const int BN = moe_gemm_bn(E, N, T);
     const MoeSizes z = moe_sizes(DT, E, M, K, N, T, BN, !SWI);
     uint8_t *p = static_cast<uint8_t *>(work);
@@ -887,13 +927,16 @@ hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_
     a.mat_bytes = M * a.row_bytes;
     a.K = (int)K;
     a.nkt = (int)z.nkt;
-    a.mtiles = (int)((M + (SWI ? 32 : 64) * W - 1) / ((SWI ? 32 : 64) * W));
+    a.mtiles = (int)z.mtiles;
+    a.splits = (int)z.splits;
+    a.kper = (int)z.kper;
     a.T = SWI ? (int)T : 1;
     for (int64_t n0 = 0; n0 < N; n0 += z.tokens) {
         const int64_t n = std::min(z.tokens, N - n0), S = n * T, rows = SWI ? n : S;
         const int32_t *idc = ids + n0 * T;
         a.xs_bytes = (uint32_t)(rows * z.nkt * KT_BYTES);
-        a.out = SWI ? out + n0 * T * M : a.ws.prod;
+        a.out = SWI ? out + n0 * T * M : nullptr;
+        a.part_stride = (SWI ? 2 : 1) * S * M;
         const dim3 pg((unsigned)((rows + 7) / 8 + 1));
         const float *xc = X + n0 * (SWI ? 1 : T) * K;
         if (K <= 4096)
@@ -905,14 +948,18 @@ hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_
         const int64_t tiles = S / BN + std::min(E, S);
         if (BN == 32) launch_gemm<DT, 1, W, SWI>(a, tiles, st);
         else launch_gemm<DT, 2, W, SWI>(a, tiles, st);
+        if (SWI && a.splits > 1) {
+            const dim3 sg((unsigned)S, (unsigned)std::min<int64_t>((M + 255) / 256, 64));
+            hipLaunchKernelGGL(moe_silu_parts_kernel, sg, dim3(256), 0, st, idc, a.ws.prod, a.out, (int)E, M, a.splits, a.part_stride);
+        }
         if (!SWI) {
             const float *res = residual ? residual + n0 * M : nullptr;
             float *y = out + n0 * M;
             const bool vec = M % 4 == 0 && ((uintptr_t)res & 15) == 0 && ((uintptr_t)y & 15) == 0;
             const int64_t per = vec ? 1024 : 256;
             const dim3 cg((unsigned)n, (unsigned)std::min<int64_t>((M + per - 1) / per, 64));
-            if (vec) hipLaunchKernelGGL((moe_combine_kernel<4>), cg, dim3(256), 0, st, idc, weights + n0 * T, a.ws.prod, res, y, (int)E, M, (int)T);
-            else hipLaunchKernelGGL((moe_combine_kernel<1>), cg, dim3(256), 0, st, idc, weights + n0 * T, a.ws.prod, res, y, (int)E, M, (int)T);
+            if (vec) hipLaunchKernelGGL((moe_combine_kernel<4>), cg, dim3(256), 0, st, idc, weights + n0 * T, a.ws.prod, res, y, (int)E, M, (int)T, a.splits, a.part_stride);
+            else hipLaunchKernelGGL((moe_combine_kernel<1>), cg, dim3(256), 0, st, idc, weights + n0 * T, a.ws.prod, res, y, (int)E, M, (int)T, a.splits, a.part_stride);
         }
     }
     return hipGetLastError();

@@ -93,12 +93,13 @@ def test_moe_down_rejects(kw, code):
 
 
 @pytest.mark.parametrize("call,need", [(swiglu, q.moe_swiglu_work_bytes), (down, q.moe_down_work_bytes)])
-@pytest.mark.parametrize("dims", [(2, 8, 64, 256, 512, 2), (14, 64, 1024, 2048, 512, 8), (8, 4, 63, 96, 3, 1)])
-def test_moe_work_is_checked(call, need, dims):
+@pytest.mark.parametrize("dims,some", [((2, 8, 1024, 4096, 512, 2), True), ((14, 64, 1024, 2048, 512, 8), True),
+                                       ((8, 4, 63, 96, 3, 1), False), ((12, 8, 14336, 4096, 1, 2), False)])
+def test_moe_work_is_checked(call, need, dims, some):
     dtype, E, M, K, N, T = dims
     kw = dict(dtype=dtype, E=E, M=M, K=K, N=N, T=T)
     n = need(*dims)
-    assert n >= 0
+    assert (n > 0) == some  # few tokens need no workspace
     if n:
         assert call(work=0, work_bytes=0, **kw) == q.QMM_ERR_NULL
         assert call(work=A + 8, work_bytes=n, **kw) == q.QMM_ERR_ALIGN

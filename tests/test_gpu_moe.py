@@ -142,6 +142,58 @@ def test_long_rows(dt):
         check_swiglu(dt, 2, 33, K, 40, 2)
 
 
+def tokens_on_matrix_cores(need, dt, E, M, K, T, start=1):
+    """The fewest tokens (from `start`) that run the matrix-core form: the one with a workspace."""
+    lo, hi = start - 1, start
+    while need(dt, E, M, K, hi, T) == 0:
+        lo, hi = hi, 2 * hi
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (lo, mid) if need(dt, E, M, K, mid, T) else (mid, hi)
+    return hi
+
+
+# (E, T, M, K in blocks of 32 or 256): one weight block per row, odd block counts,
+# rows that are not a multiple of a fragment or a workgroup, K that the workgroups share
+MANY = [(1, 1, 1, 1), (3, 2, 5, 3), (2, 1, 33, 2), (5, 3, 70, 5), (4, 2, 257, 4), (2, 2, 130, 17)]
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+@pytest.mark.parametrize("E,T,M,blocks", MANY)
+def test_many_tokens(dt, E, T, M, blocks):
+    K = blocks * GEOMETRY[dt][0]
+    N = tokens_on_matrix_cores(q.moe_swiglu_work_bytes, dt, E, M, K, T)
+    g = np.random.default_rng(N)
+    ids = g.integers(-1, E + 1, (N, T), dtype=np.int32)   # some slots without an expert
+    check_swiglu(dt, E, M, K, N, T, ids=ids)
+    N = tokens_on_matrix_cores(q.moe_down_work_bytes, dt, E, M, K, T)
+    check_down(dt, E, M, K, N, T, ids=g.integers(-1, E + 1, (N, T), dtype=np.int32), in_place=M % 2 == 0)
+    check_down(dt, E, M, K, N + 1, T, residual=False)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+def test_few_slots_per_expert_on_matrix_cores(dt):
+    """Tiles of 32 slots, most of them partly filled; experts with none, one, 32 and 33 slots."""
+    E, T, M, K = 16, 2, 500, 2048
+    for need, check in ((q.moe_swiglu_work_bytes, check_swiglu), (q.moe_down_work_bytes, check_down)):
+        N = tokens_on_matrix_cores(need, dt, E, M, K, T, start=70)
+        ids = np.full(N * T, -1, np.int32)
+        ids[:33], ids[33:65], ids[65], ids[66:N * T - 5] = 3, 9, 15, 0
+        g = np.random.default_rng(2)
+        check(dt, E, M, K, N, T, ids=g.permutation(ids))
+        check(dt, E, M, K, N, T)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
+def test_shared_k_on_matrix_cores(dt):
+    """Long rows and few of them: workgroups share a row's k-tiles."""
+    for M, K in ((300, 14336), (40, 16640)):
+        N = tokens_on_matrix_cores(q.moe_swiglu_work_bytes, dt, 2, M, K, 2)
+        check_swiglu(dt, 2, M, K, N, 2)
+        N = tokens_on_matrix_cores(q.moe_down_work_bytes, dt, 2, M, K, 2)
+        check_down(dt, 2, M, K, N, 2)
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 8, 9, 31, 32])
 def test_slots_per_token(T):
     for N in (1, 2, 40):
@@ -166,23 +218,23 @@ def test_padding_and_uneven_experts(dt, N):
 
 
 @pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
-@pytest.mark.parametrize("N", [1, 48])
-def test_scales_of_activations(dt, N):
+@pytest.mark.parametrize("many", [False, True])
+def test_scales_of_activations(dt, many):
     """Rows of very different magnitudes beside each other, and within a row."""
     E, M, K, T = 3, 40, 512, 2
+    N = tokens_on_matrix_cores(q.moe_swiglu_work_bytes, dt, E, M, K, T) * 2 if many else 48
     g = np.random.default_rng(5)
     X = make_x(N * T, K, g)
     X *= (10.0 ** g.uniform(-12, 12, (N * T, 1))).astype(np.float32)
     X[:, ::7] *= 1e-3
     X[0, :] = 0.0
-    X[N * T - 1] *= 0.0 if N == 1 else 1.0
     check_down(dt, E, M, K, N, T, H=X)
-    check_swiglu(dt, E, M, K, N, T, X=np.ascontiguousarray(X[:N]) if N > 1 else 1e-4 * make_x(1, K, g))
+    check_swiglu(dt, E, M, K, N, T, X=np.ascontiguousarray(X[:N]))
 
 
 def test_non_finite_rows_stay_in_their_token():
     dt, E, M, K, T = q.QMM_Q4_K, 3, 64, 512, 2
-    for N in (4, 64):
+    for N in (4, 64, tokens_on_matrix_cores(q.moe_swiglu_work_bytes, dt, E, M, K, T)):
         g = np.random.default_rng(6)
         ids = g.integers(0, E, (N, T), dtype=np.int32)
         G, U, X = experts(dt, E, M, K, 0), experts(dt, E, M, K, 1), make_x(N, K, g)
@@ -198,19 +250,20 @@ def test_non_finite_rows_stay_in_their_token():
 @pytest.mark.parametrize("dt", DTYPES, ids=lambda d: NAMES[d])
 def test_results_repeat_and_do_not_hang_on_neighbours(dt):
     """Bitwise: run to run, and for a token moved elsewhere among the same tokens."""
-    E, M, K, T, N = 5, 96, 1024, 3, 70
-    g = np.random.default_rng(8)
-    ids, X = g.integers(0, E, (N, T), dtype=np.int32), make_x(N, K, g)
-    G, U = dev(experts(dt, E, M, K, 0)), dev(experts(dt, E, M, K, 1))
-    a = run_swiglu(dt, E, M, K, N, T, dev(ids), G, U, dev(X)).clone()
-    b = run_swiglu(dt, E, M, K, N, T, dev(ids), G, U, dev(X)).clone()
-    p = g.permutation(N)
-    c = run_swiglu(dt, E, M, K, N, T, dev(ids[p]), G, U, dev(X[p]))
-    assert torch.equal(a, b)
-    assert torch.equal(a.view(N, T, M)[torch.from_numpy(p).cuda()], c.view(N, T, M))
+    E, M, K, T = 5, 96, 1024, 3
+    for N in (70, tokens_on_matrix_cores(q.moe_swiglu_work_bytes, dt, E, M, K, T)):
+        g = np.random.default_rng(8)
+        ids, X = g.integers(0, E, (N, T), dtype=np.int32), make_x(N, K, g)
+        G, U = dev(experts(dt, E, M, K, 0)), dev(experts(dt, E, M, K, 1))
+        a = run_swiglu(dt, E, M, K, N, T, dev(ids), G, U, dev(X)).clone()
+        b = run_swiglu(dt, E, M, K, N, T, dev(ids), G, U, dev(X)).clone()
+        p = g.permutation(N)
+        c = run_swiglu(dt, E, M, K, N, T, dev(ids[p]), G, U, dev(X[p]))
+        assert torch.equal(a, b)
+        assert torch.equal(a.view(N, T, M)[torch.from_numpy(p).cuda()], c.view(N, T, M))
 
 
-@pytest.mark.parametrize("N", [1, 9, 96])
+@pytest.mark.parametrize("N", [1, 9, 96, 640])
 def test_block_together(N):
     """norm -> router product -> routing -> experts -> sum with the residual ->
     next norm as Q8_0 -> the int8 product, eager on a side stream, then
@@ -226,6 +279,7 @@ def test_block_together(N):
     e = lambda *s, dtype=torch.float32: torch.empty(s, device="cuda", dtype=dtype)
     x1, h, lg, ids, wt = e(N, K), e(N, K), e(N, E), e(N, T, dtype=torch.int32), e(N, T)
     act, x2, sc, qq, y = e(N, T, M), e(N, K), e(N, K // 32), e(N, K, dtype=torch.int8), e(N, 64)
+    assert (q.moe_swiglu_work_bytes(dt, E, M, K, N, T) > 0) == (N >= 96)  # both forms
     ws = work_of(q.moe_swiglu_work_bytes(dt, E, M, K, N, T))
     wd = work_of(q.moe_down_work_bytes(q.QMM_Q6_K, E, K, M, N, T))
     outs = (x1, h, lg, ids, wt, act, x2, sc, qq, y)
