@@ -214,7 +214,7 @@ def _addr(t, nbytes: int | None, what: str, torch_dtype=None) -> int:
         raise ValueError(f"{what} must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if torch_dtype is not None and t.dtype != torch_dtype:
+    if torch_dtype is not None and t.dtype is not torch_dtype:
         raise ValueError(f"{what} must be {torch_dtype}, got {t.dtype}")
     if nbytes is not None and t.nbytes < nbytes:
         raise ValueError(f"{what} holds {t.nbytes} bytes, needs {nbytes}")

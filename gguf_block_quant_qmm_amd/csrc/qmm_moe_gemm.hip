@@ -339,14 +339,21 @@ struct MoeWs {
 // BN; the order of slots within an expert moves no result (every output row
 // depends on its own activation row alone).
 __device__ void plan_tiles(const int32_t *ids, int S, int E, int BN, int4 *tiles, int32_t *order) {
-    __shared__ int count[MOE_E_MAX], start[MOE_E_MAX + 1], tile0[MOE_E_MAX + 1];
+    __shared__ int count[MOE_E_MAX], start[MOE_E_MAX], tile0[MOE_E_MAX];
     const int t = (int)threadIdx.x, T = (int)blockDim.x;
+    // the first slots' ids stay in registers between the two passes
+    constexpr int KEEP = 16;
+    int mine[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; i++) mine[i] = t + i * T < S ? ids[t + i * T] : -1;
     for (int e = t; e < E; e += T) count[e] = 0;
     __syncthreads();
-    for (int s = t; s < S; s += T) {
-        const int e = ids[s];
+    auto add = [&](int e) {
         if (e >= 0 && e < E) atomicAdd(&count[e], 1);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; i++) add(mine[i]);
+    for (int s = t + KEEP * T; s < S; s += T) add(ids[s]);
     __syncthreads();
     if (t < 64) {  // one wavefront: exclusive sums over the experts, 64 at a time
         int base = 0, tbase = 0;
@@ -369,15 +376,17 @@ __device__ void plan_tiles(const int32_t *ids, int S, int E, int BN, int4 *tiles
     }
     __syncthreads();
     for (int e = t; e < E; e += T) {
-        const int c = count[e];
-        for (int i = 0; i * BN < c; i++)
-            tiles[1 + tile0[e] + i] = int4{e, start[e] + i * BN, (c - i * BN < BN ? c - i * BN : BN) | ((c + BN - 1) / BN) << 8, tile0[e]};
+        const int c = count[e], s0 = start[e], tc = (c + BN - 1) / BN;
+        for (int i = 0; i < tc; i++)
+            tiles[1 + tile0[e] + i] = int4{e, s0 + i * BN, (c - i * BN < BN ? c - i * BN : BN) | tc << 8, tile0[e]};
     }
     __syncthreads();
-    for (int s = t; s < S; s += T) {
-        const int e = ids[s];
+    auto put = [&](int s, int e) {
         if (e >= 0 && e < E) order[atomicAdd(&start[e], 1)] = s;
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; i++) put(t + i * T, mine[i]);
+    for (int s = t + KEEP * T; s < S; s += T) put(s, ids[s]);
 }
 
 // One piece (8 values, in the operand order) of a split row: 16 bytes of hi, 16 of lo.
@@ -418,35 +427,38 @@ __device__ __forceinline__ void put_piece(const MoeWs &ws, int64_t row, int nkt,
     }
 }
 
-// Workgroup 0 plans the tiles; a wavefront of the others splits one row.  REG:
-// the row (up to 4096 values) stays in registers between the maximum and the
-// split; else it is read twice.  zero_out (gate/up): the output rows [M] of a
-// token's slots without an expert are cleared here, for the GEMM writes only
-// rows that have one.  slot_rows (down): rows are slots, and those without an
-// expert are skipped.
-template <int DT, bool REG>
-__global__ void __launch_bounds__(512) moe_prep_kernel(const int32_t *ids, int S, int E, int BN, MoeWs ws, const float *X,
+// Workgroup 0 plans the tiles; the others split rows, WPR of their 4 wavefronts
+// on each.  REG: a row (K <= 1024 WPR) stays in registers between its maximum
+// and the split; else it is read twice.  zero_out (gate/up): the output rows [M]
+// of a token's slots without an expert are cleared here, for the GEMM writes
+// only rows that have one.  slot_rows (down): rows are slots, and those without
+// an expert are skipped.
+template <int DT, int WPR, bool REG>
+__global__ void __launch_bounds__(256) moe_prep_kernel(const int32_t *ids, int S, int E, int BN, MoeWs ws, const float *X,
                                                        int64_t rows, int K, int nkt, int T, bool slot_rows, float *zero_out,
                                                        int64_t M) {
     if (blockIdx.x == 0) {
         plan_tiles(ids, S, E, BN, ws.tiles, ws.order);
         return;
     }
-    const int lane = (int)threadIdx.x & 63;
-    const int64_t row = ((int64_t)blockIdx.x - 1) * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    if (row >= rows) return;
-    if (slot_rows) {
+    __shared__ float red[4];
+    constexpr int TPR = 64 * WPR;  // threads per row
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), t = (int)threadIdx.x % TPR;
+    const int64_t row = ((int64_t)blockIdx.x - 1) * (4 / WPR) + wave / WPR;
+    const bool in = row < rows;
+    bool live = in;
+    if (in && slot_rows) {
         const int e = ids[row];
-        if (e < 0 || e >= E) return;
-    } else {
-        for (int t = 0; t < T; t++) {
-            const int e = ids[row * T + t];
+        live = e >= 0 && e < E;
+    } else if (in) {
+        for (int i = 0; i < T; i++) {
+            const int e = ids[row * T + i];
             if (e < 0 || e >= E)
-                for (int64_t m = lane; m < M; m += 64) zero_out[(row * T + t) * M + m] = 0.f;
+                for (int64_t m = t; m < M; m += TPR) zero_out[(row * T + i) * M + m] = 0.f;
         }
     }
     const int n = nkt * 16;  // pieces; lanes of a 16-lane group are in or out together
-    const Rsrc rs = make_rsrc_uniform(X + row * K, 4u * (uint32_t)K);  // zeros past the row
+    const Rsrc rs = make_rsrc_uniform(X + (live ? row : 0) * K, live ? 4u * (uint32_t)K : 0u);  // zeros past the row
     float amax = 0.f;
     auto fold = [&](const floatx4 &v) {
 #pragma unroll
@@ -460,15 +472,15 @@ __global__ void __launch_bounds__(512) moe_prep_kernel(const int32_t *ids, int S
         a = __builtin_bit_cast(floatx4, ld128(rs, k, 0));
         b = __builtin_bit_cast(floatx4, ld128(rs, k + 16u, 0));
     };
-    constexpr int PPL = REG ? 8 : 1;
+    constexpr int PPL = 2;
     floatx4 va[PPL], vb[PPL];
     if constexpr (REG) {
 #pragma unroll
-        for (int j = 0; j < PPL; j++) load(lane + 64 * j, va[j], vb[j]);
+        for (int j = 0; j < PPL; j++) load(t + TPR * j, va[j], vb[j]);
 #pragma unroll
         for (int j = 0; j < PPL; j++) { fold(va[j]); fold(vb[j]); }
     } else {
-        for (int i = lane; i < n; i += 64) {
+        for (int i = t; i < n; i += TPR) {
             load(i, va[0], vb[0]);
             fold(va[0]);
             fold(vb[0]);
@@ -476,19 +488,26 @@ __global__ void __launch_bounds__(512) moe_prep_kernel(const int32_t *ids, int S
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
+    if constexpr (WPR > 1) {
+        if ((threadIdx.x & 63) == 0) red[wave] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WPR; w++) amax = fmaxf(amax, red[wave / WPR * WPR + w]);
+    }
+    if (!live) return;
     // amax = f * 2^e, f in [0.5, 1): multiply by 2^(10 - e)
     int e = 0;
     (void)frexpf(amax, &e);
     int m = amax > 0.f ? 10 - e : 0;
     m = m > 126 ? 126 : m;
     const float mul = ldexpf(1.0f, m);
-    if (lane == 0) ws.rscale[row] = ldexpf(1.0f, -m);
+    if (t == 0) ws.rscale[row] = ldexpf(1.0f, -m);
     if constexpr (REG) {
 #pragma unroll
         for (int j = 0; j < PPL; j++)
-            if (lane + 64 * j < n) put_piece<DT>(ws, row, nkt, lane + 64 * j, va[j], vb[j], mul);
+            if (t + TPR * j < n) put_piece<DT>(ws, row, nkt, t + TPR * j, va[j], vb[j], mul);
     } else {
-        for (int i = lane; i < n; i += 64) {
+        for (int i = t; i < n; i += TPR) {
             load(i, va[0], vb[0]);
             put_piece<DT>(ws, row, nkt, i, va[0], vb[0], mul);
         }
@@ -514,7 +533,10 @@ struct MoeGemmArgs {
 // them in its part of LDS one k-tile ahead and reads each lane's bytes from
 // there.  Activations: all wavefronts share the tile's rows, double-buffered.
 template <int DT, int FN, int W, bool SWI>
-__global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a) {
+#ifndef OCC1
+#define OCC1 2
+#endif
+__global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(const MoeGemmArgs a) {
     using D = MDec<DT>;
     constexpr int BN = 32 * FN, RW = SWI ? 32 : 64, BM = RW * W;
     constexpr int NP = BN * 16 / (64 * W);  // 16-byte pieces of half a k-tile per thread
@@ -937,14 +959,17 @@ hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_
         a.xs_bytes = (uint32_t)(rows * z.nkt * KT_BYTES);
         a.out = SWI ? out + n0 * T * M : nullptr;
         a.part_stride = (SWI ? 2 : 1) * S * M;
-        const dim3 pg((unsigned)((rows + 7) / 8 + 1));
         const float *xc = X + n0 * (SWI ? 1 : T) * K;
-        if (K <= 4096)
-            hipLaunchKernelGGL((moe_prep_kernel<DT, true>), pg, dim3(512), 0, st, idc, (int)S, (int)E, BN, a.ws, xc, rows, (int)K,
-                               (int)z.nkt, (int)T, !SWI, a.out, M);
-        else
-            hipLaunchKernelGGL((moe_prep_kernel<DT, false>), pg, dim3(512), 0, st, idc, (int)S, (int)E, BN, a.ws, xc, rows, (int)K,
-                               (int)z.nkt, (int)T, !SWI, a.out, M);
+        const int wpr = K <= 1024 ? 1 : K <= 2048 ? 2 : 4;  // wavefronts per row
+        const dim3 pg((unsigned)((rows * wpr + 3) / 4 + 1));
+#define QMM_PREP(WPR, REG)                                                                                              \
+    hipLaunchKernelGGL((moe_prep_kernel<DT, WPR, REG>), pg, dim3(256), 0, st, idc, (int)S, (int)E, BN, a.ws, xc, rows, (int)K, \
+                       (int)z.nkt, (int)T, !SWI, a.out, M)
+        if (wpr == 1) QMM_PREP(1, true);
+        else if (wpr == 2) QMM_PREP(2, true);
+        else if (K <= 4096) QMM_PREP(4, true);
+        else QMM_PREP(4, false);
+#undef QMM_PREP
         const int64_t tiles = S / BN + std::min(E, S);
         if (BN == 32) launch_gemm<DT, 1, W, SWI>(a, tiles, st);
         else launch_gemm<DT, 2, W, SWI>(a, tiles, st);

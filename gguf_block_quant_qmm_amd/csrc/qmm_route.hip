@@ -7,9 +7,10 @@
 //
 // A wavefront per token.  Scores and choices are f64: which expert is chosen
 // next to a border must not hang on the last bits of an f32 exponential, and
-// a token's few hundred exponentials are hidden behind the launch.  A choice
-// is compared as a 64-bit integer that orders like the f64 value, so one
-// maximum over the wavefront is two DPP moves and a compare per step.
+// a token's few hundred exponentials are hidden behind the launch.  The
+// running choices are f64 values with NaN for an expert that is out (chosen, or
+// in a closed group): v_max_f64 passes over NaN, so a maximum over the
+// wavefront is two DPP moves and one instruction per step.
 #include "qmm_device.hpp"
 #include "qmm_internal.hpp"
 
@@ -27,35 +28,26 @@ struct RouteArgs {
     double scale;
 };
 
-// An integer that orders like v; NaN counts as -inf; 0 is below everything.
-__device__ __forceinline__ uint64_t order_key(double v) {
-    if (v != v) v = -__builtin_inf();
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_max(double v) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+    // lanes without a source keep their own value
+    const uint32_t lo = __builtin_amdgcn_update_dpp((int)(uint32_t)b, (int)(uint32_t)b, CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp((int)(uint32_t)(b >> 32), (int)(uint32_t)(b >> 32), CTRL, ROW_MASK, 0xF, false);
+    return fmax(v, __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo));
 }
-
-template <int CTRL, int ROW_MASK, bool BOUND>
-__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROW_MASK, 0xF, BOUND);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROW_MASK, 0xF, BOUND);
-    return ((uint64_t)hi << 32) | lo;
-}
-__device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int lane) {
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
-    return ((uint64_t)hi << 32) | lo;
-}
-__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-
-// The wavefront's largest key, uniform (0, the identity, where DPP reads nothing).
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-    v = max_u64(v, dpp_u64<0xB1, 0xF, true>(v));    // quad_perm 1,0,3,2
-    v = max_u64(v, dpp_u64<0x4E, 0xF, true>(v));    // quad_perm 2,3,0,1
-    v = max_u64(v, dpp_u64<0x141, 0xF, true>(v));   // row_half_mirror
-    v = max_u64(v, dpp_u64<0x140, 0xF, true>(v));   // row_mirror
-    v = max_u64(v, dpp_u64<0x142, 0xA, false>(v));  // row_bcast15
-    v = max_u64(v, dpp_u64<0x143, 0xC, false>(v));  // row_bcast31
-    return readlane_u64(v, 63);
+// The wavefront's largest value (NaN only if all are), uniform.
+__device__ __forceinline__ double wave_max_d(double v) {
+    v = dpp_max<0xB1, 0xF>(v);   // quad_perm 1,0,3,2
+    v = dpp_max<0x4E, 0xF>(v);   // quad_perm 2,3,0,1
+    v = dpp_max<0x141, 0xF>(v);  // row_half_mirror
+    v = dpp_max<0x140, 0xF>(v);  // row_mirror
+    v = dpp_max<0x142, 0xA>(v);  // row_bcast15
+    v = dpp_max<0x143, 0xC>(v);  // row_bcast31: the maximum, in lane 63
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 __device__ __forceinline__ double wave_sum_d(double v) {
 #pragma unroll
@@ -71,8 +63,8 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t n = (int64_t)blockIdx.x * (blockDim.x >> 6) + wave;
     const bool grouped = a.groups > a.topk_groups;  // else every group stays open
-    double *ss = lds + (size_t)wave * (64 * EPL + (grouped ? 64 * EPL + a.groups : 0));
-    double *cs = ss + 64 * EPL, *gs = cs + 64 * EPL;  // grouped only
+    double *ss = lds + (size_t)wave * (64 * EPL + (grouped ? 64 * EPL + 2 * a.groups : 0));
+    double *cs = ss + 64 * EPL, *gs = cs + 64 * EPL, *gopen = gs + a.groups;  // grouped only
     const bool live = n < a.N;                         // uniform per wavefront
 
     float l[EPL];
@@ -103,61 +95,79 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
 #pragma unroll
         for (int i = 0; i < EPL; i++) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
     }
-    uint64_t key[EPL];
+    const double out = __builtin_nan("");
 #pragma unroll
     for (int i = 0; i < EPL; i++) {
         const int e = 64 * i + lane;
         c[i] = s[i] + ((a.bias && e < a.E) ? (double)a.bias[e] : 0.0);
-        key[i] = e < a.E ? order_key(c[i]) : 0;
+        if (c[i] != c[i]) c[i] = -__builtin_inf();
         ss[e] = s[i];
+        if (grouped) cs[e] = c[i];
+        if (e >= a.E) c[i] = out;
     }
+    __syncthreads();
     if (grouped) {
-#pragma unroll
-        for (int i = 0; i < EPL; i++) cs[64 * i + lane] = c[i] != c[i] ? -__builtin_inf() : c[i];
-        __syncthreads();
+        // group g on the 64 / groups (a power of two) lanes g * parts ..: each
+        // scans every parts-th expert for its two largest, then they merge
         const int gsz = a.E / a.groups;
-        for (int g = lane; g < a.groups; g += 64) {
+        int parts = 1;
+        while (2 * parts * a.groups <= 64) parts *= 2;
+        for (int g0 = 0; g0 < a.groups; g0 += 64) {
+            const int g = g0 + lane / parts, part = lane % parts;
             double m1 = -__builtin_inf(), m2 = -__builtin_inf();
-            for (int j = 0; j < gsz; j++) {
-                const double v = cs[g * gsz + j];
-                m2 = v > m1 ? m1 : (v > m2 ? v : m2);
-                m1 = v > m1 ? v : m1;
+            if (g < a.groups) {
+                for (int j = part; j < gsz; j += parts) {
+                    const double v = cs[g * gsz + j];
+                    m2 = fmax(m2, fmin(m1, v));
+                    m1 = fmax(m1, v);
+                }
             }
-            const double v = a.group_top == 2 ? m1 + m2 : m1;
-            gs[g] = v != v ? -__builtin_inf() : v;
+            for (int o = 1; o < parts; o *= 2) {
+                const double n1 = __shfl_xor(m1, o, 64), n2 = __shfl_xor(m2, o, 64);
+                m2 = fmax(fmin(m1, n1), fmax(m2, n2));
+                m1 = fmax(m1, n1);
+            }
+            if (g < a.groups && part == 0) {
+                const double v = a.group_top == 2 ? m1 + m2 : m1;
+                gs[g] = v != v ? -__builtin_inf() : v;
+            }
         }
         __syncthreads();
-        // a group stays open if fewer than topk_groups groups come before it
+        // a group stays open if fewer than topk_groups groups come before it;
+        // a closed one is marked by a NaN where its score was
+        for (int g0 = 0; g0 < a.groups; g0 += 64) {
+            const int g = g0 + lane;
+            int before = 0;
+            if (g < a.groups) {
+                const double mine = gs[g];
+                for (int o = 0; o < a.groups; o++) before += (gs[o] > mine || (gs[o] == mine && o < g)) ? 1 : 0;
+            }
+            if (g < a.groups) gopen[g] = before < a.topk_groups ? 0.0 : out;
+        }
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            const int e = 64 * i + lane, g = e / gsz;
-            if (e < a.E) {
-                const double mine = gs[g];
-                int before = 0;
-                for (int o = 0; o < a.groups; o++) before += (gs[o] > mine || (gs[o] == mine && o < g)) ? 1 : 0;
-                if (before >= a.topk_groups) key[i] = 0;
-            }
+            const int e = 64 * i + lane;
+            if (e < a.E && gopen[e / gsz] != 0.0) c[i] = out;
         }
-    } else {
-        __syncthreads();  // ss
     }
-    // the largest key, topk times; equal keys: the smallest index
+    // the largest choice, topk times; equal ones: the smallest index
     int chosen = 0;  // lane k: the k-th expert
     for (int k = 0; k < a.topk; k++) {
-        uint64_t mine = 0;
+        double mine = c[0];
 #pragma unroll
-        for (int i = 0; i < EPL; i++) mine = max_u64(mine, key[i]);
-        const uint64_t top = wave_max_u64(mine);
-        int e = -1;
+        for (int i = 1; i < EPL; i++) mine = fmax(mine, c[i]);
+        const double top = wave_max_d(mine);
+        int e = 0;
 #pragma unroll
         for (int i = EPL - 1; i >= 0; i--) {
-            const uint64_t at = __ballot(key[i] == top);
+            const uint64_t at = __ballot(c[i] == top);
             if (at) e = 64 * i + __ffsll((unsigned long long)at) - 1;
         }
         if (lane == k) chosen = e;
 #pragma unroll
         for (int i = 0; i < EPL; i++)
-            if (e == 64 * i + lane) key[i] = 0;
+            if (e == 64 * i + lane) c[i] = out;
     }
     double w = lane < a.topk ? ss[chosen] : 0.0;
     if (a.renorm) {
@@ -192,7 +202,7 @@ hipError_t launch_moe_route(const float *logits, const float *bias, int64_t N, i
     const int epl = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16;
     // four tokens per workgroup while their scores stay below 64 KB of LDS
     const unsigned wpb = epl > 4 ? 1 : (N >= 4 ? 4 : (unsigned)N);
-    const size_t lds = 8 * (size_t)wpb * (64 * epl + (groups > topk_groups ? 64 * epl + groups : 0));
+    const size_t lds = 8 * (size_t)wpb * (64 * epl + (groups > topk_groups ? 64 * epl + 2 * groups : 0));
     const dim3 grid((unsigned)((N + wpb - 1) / wpb)), block(64 * wpb);
     switch (epl) {
     case 1: hipLaunchKernelGGL((route_kernel<1>), grid, block, lds, st, a); break;
