@@ -141,7 +141,7 @@ template <> struct MDec<QMM_Q4_1> {
         return b < nb ? h2f(r[3 * b + 2]) : 0.f;
     }
     static constexpr bool PAIR = false;  // every k-tile; the minima stand for themselves (scale 1)
-    __device__ static half8 offset(const uint32_t (&)[NW], int, const Pre &p, float &) {
+    __device__ static half8 offset(const uint8_t *, int, const Pre &p, float &) {
         const half2v a = h2(p.m[0] | (p.m[2] << 16)), c = h2(p.m[1] | (p.m[3] << 16));
         return join(a, c, a, c);
     }
@@ -242,9 +242,10 @@ struct MDecK {
     // the minima of the whole super-block in one step, after its second k-tile:
     // lane half kh holds those of k-tile kh
     static constexpr bool PAIR = true;
-    __device__ static half8 offset(const uint32_t (&r)[NW], int kh, const Pre &, float &so) {
-        const uint32_t mn = k_mins4(r[2], r[3], (uint32_t)-kh);
-        so = -h2f(r[0] >> 16);
+    __device__ static half8 offset(const uint8_t *p, int kh, const Pre &, float &so) {
+        const u32x4_t h = at128(p + ROW - 16);  // the header again, from LDS: no registers held for it
+        const uint32_t mn = k_mins4(h.z, h.w, (uint32_t)-kh);
+        so = -h2f(h.x >> 16);
         const half2v m = byte02_code(mn, 0.f), n = byte13_code(mn, 0.f);  // [m0 m2], [m1 m3]
         return join(m, n, m, n);
     }
@@ -275,7 +276,7 @@ template <> struct MDec<QMM_Q5_K> : MDecK<1> {};
 template <> struct MDec<QMM_Q6_K> {
     static constexpr int NW = 15, STEPS = 1, NG = 2;
     static constexpr bool OFF = false;
-    struct Pre { float s[8]; };
+    struct Pre { float d; };
     __host__ __device__ static constexpr int step(int i) { return 2 * (i & 3) + (i >> 2); }
     __host__ __device__ static int kbase(int p) { return 16 * step(p >> 1) + 8 * (p & 1); }
     __host__ __device__ static float xscale(int) { return 1.0f; }
@@ -304,11 +305,11 @@ template <> struct MDec<QMM_Q6_K> {
         }
     }
     __device__ static void prep(const uint32_t (&r)[NW], int, int, Pre &p) {
-        const float d = h2f(r[14]);
-#pragma unroll
-        for (int i = 0; i < 8; i++) p.s[i] = d * (float)(int)(int8_t)(uint8_t)(r[12 + (i >> 2)] >> (8 * (i & 3)));
+        p.d = h2f(r[14]);
     }
-    __device__ static float scale(const uint32_t (&)[NW], int st, int, const Pre &p) { return p.s[st]; }
+    __device__ static float scale(const uint32_t (&r)[NW], int st, int, const Pre &p) {
+        return p.d * (float)(int)(int8_t)(uint8_t)(r[12 + (st >> 2)] >> (8 * (st & 3)));
+    }
     __device__ static half8 frag(const uint32_t (&r)[NW], int st, int, const Pre &) {
         const int g = st >> 1, li = st & 1;
         uint32_t q[2];
@@ -533,10 +534,7 @@ struct MoeGemmArgs {
 // them in its part of LDS one k-tile ahead and reads each lane's bytes from
 // there.  Activations: all wavefronts share the tile's rows, double-buffered.
 template <int DT, int FN, int W, bool SWI>
-#ifndef OCC1
-#define OCC1 2
-#endif
-__global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(const MoeGemmArgs a) {
+__global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a) {
     using D = MDec<DT>;
     constexpr int BN = 32 * FN, RW = SWI ? 32 : 64, BM = RW * W;
     constexpr int NP = BN * 16 / (64 * W);  // 16-byte pieces of half a k-tile per thread
@@ -573,15 +571,15 @@ __global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(co
     // activation pieces: piece c of thread t is 16-byte piece t % 16 of row t / 16 + c (4 W),
     // kept at piece (t % 16) ^ (row % 16) in LDS: 16 rows' reads of one piece
     // fall on 16 different bank groups
+    static_assert((4 * W) % 16 == 0, "a thread's pieces lie in rows that agree modulo 16");
     uint32_t xoff[NP];
-    uint32_t xdst[NP];
+    const uint32_t xdst = (uint32_t)((t >> 4) * XT_BYTES + 16 * ((t ^ (t >> 4)) & 15));
 #pragma unroll
     for (int c = 0; c < NP; c++) {
         const int r = (t >> 4) + c * (4 * W), p = t & 15;
         const int s = slot_of[r];
         // rows past the tile's end read nothing (zeros)
         xoff[c] = s >= 0 ? (uint32_t)(s / a.T) * (uint32_t)(a.nkt * KT_BYTES) + 16u * p : 0xFFFFFFF0u - (uint32_t)(a.nkt * KT_BYTES);
-        xdst[c] = (uint32_t)(r * XT_BYTES + 16 * ((p ^ r) & 15));
     }
     const Rsrc xrs = make_rsrc_uniform(a.ws.xs, a.xs_bytes);
 
@@ -601,12 +599,13 @@ __global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(co
     uint8_t *const wrow[2] = {&wl[wave][l32 * D::ROW], &wl[wave][(32 + l32) * D::ROW]};
 
     // block sums of the lane's slots (formats with minima): lane half 0 alone
-    const uint4 *sump[FN];
+    uint32_t sumoff[FN];
+    const Rsrc srs = make_rsrc_uniform(a.ws.sums, D::OFF ? a.xs_bytes / (KT_BYTES / 16) : 0u);
     if constexpr (D::OFF) {
 #pragma unroll
         for (int f = 0; f < FN; f++) {
             const int s = slot_of[32 * f + l32];
-            sump[f] = a.ws.sums + (int64_t)(s >= 0 ? s / a.T : 0) * a.nkt;
+            sumoff[f] = 16u * ((uint32_t)(s >= 0 ? s / a.T : 0) * (uint32_t)a.nkt + (D::PAIR ? (uint32_t)kh : 0u));
         }
     }
 
@@ -664,7 +663,7 @@ __global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(co
     };
     auto store_x = [&](int buf) {
 #pragma unroll
-        for (int c = 0; c < NP; c++) *reinterpret_cast<u32x4_t *>(&xl[buf][xdst[c]]) = xr[c];
+        for (int c = 0; c < NP; c++) *reinterpret_cast<u32x4_t *>(&xl[buf][xdst + c * (4 * W) * XT_BYTES]) = xr[c];
     };
     fetch_x(2 * k0);
     fetch_w(k0);
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(co
 
     for (int kt = k0; kt < k1; kt++) {
         const int kn = kt + 1 < k1 ? kt + 1 : kt;  // past the last k-tile: the last again, unused
-        uint4 so_a[FN];
+        u32x4_t so_a[FN];
         const int nb = (a.K - kt * KT) / 32;
         typename D::Pre pre[2];
         floatx16 tmp[2][FN];
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(co
                 // block sums for the step at the k-tile's (super-block's) end
                 if (n == 4 && (!D::PAIR || (kt & 1))) {
 #pragma unroll
-                    for (int f = 0; f < FN; f++) so_a[f] = sump[f][D::PAIR ? kt - 1 + kh : kt];
+                    for (int f = 0; f < FN; f++) so_a[f] = ld128(srs, sumoff[f], 16u * (uint32_t)(D::PAIR ? kt - 1 : kt));
                 }
             }
             if (n % (8 / D::NG) == 0 && n / (8 / D::NG) + 1 < D::NG) read_w(n / (8 / D::NG) + 1);
@@ -755,7 +754,7 @@ __global__ void __launch_bounds__(64 * W, FN == 1 ? OCC1 : 2) moe_gemm_kernel(co
                 for (int f = 0; f < FN; f++)
                     sa[f] = D::PAIR || kh == 0 ? __builtin_bit_cast(half8, so_a[f]) : half8{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 2; i++) off[i] = D::offset(raw[i], kh, pre[i], so[i]);
+                for (int i = 0; i < 2; i++) off[i] = D::offset(wrow[i], kh, pre[i], so[i]);
 #pragma unroll
                 for (int f = 0; f < FN; f++)
 #pragma unroll
