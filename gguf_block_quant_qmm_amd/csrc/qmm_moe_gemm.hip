@@ -882,14 +882,16 @@ __global__ void __launch_bounds__(256) moe_silu_parts_kernel(const int32_t *ids,
 // --------------------------------------------------------------- launchers ----
 constexpr int64_t align256(int64_t v) { return (v + 255) & ~(int64_t)255; }
 
-// Tokens per pass: the split rows stay below 2^31 bytes (32-bit offsets), the
-// down products below 1 GB; longer inputs run pass after pass in one workspace.
-int64_t chunk_tokens(int64_t K, int64_t M, int64_t N, int64_t T, bool down) {
-    const int64_t nkt = (K + KT - 1) / KT, row = nkt * KT_BYTES;
+// Tokens per pass: the split rows and the down products stay below 1 GB (32-bit
+// offsets), the grids below 2^32 threads; longer inputs run pass after pass in
+// one workspace.
+int64_t chunk_tokens(int64_t E, int64_t K, int64_t M, int64_t N, int64_t T, bool down) {
+    const int64_t nkt = (K + KT - 1) / KT, row = nkt * KT_BYTES, mt = M / 128 + 1;
     int64_t n = (int64_t(1) << 30) / (down ? row * T : row);
     if (down) n = std::min(n, (int64_t(1) << 30) / (4 * M * T));
-    n = std::min(n, (int64_t(1) << 22) / T);  // slots: grids of 2^32 threads
-    n = std::min(n, (int64_t(1) << 27) / T / (M / 64 + 1));  // (tiles of 32 slots) x (tiles of 128 rows) <= 2^23
+    n = std::min(n, (int64_t(1) << 22) / T);
+    // (tiles of slots: slots / 32 and one per expert with any) x (row tiles) <= 2^23
+    n = std::min(n, E * mt <= (int64_t(1) << 22) ? (int64_t(1) << 27) / (T * mt) : (int64_t(1) << 23) / (T * mt));
     return std::max<int64_t>(1, std::min(n, N));
 }
 
@@ -901,7 +903,7 @@ struct MoeSizes {
 };
 MoeSizes moe_sizes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, int BN, bool down) {
     MoeSizes z;
-    z.tokens = chunk_tokens(K, M, N, T, down);
+    z.tokens = chunk_tokens(E, K, M, N, T, down);
     z.slots = z.tokens * T;
     z.rows = down ? z.slots : z.tokens;
     z.nkt = (K + KT - 1) / KT;

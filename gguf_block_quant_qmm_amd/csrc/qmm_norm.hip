@@ -290,22 +290,28 @@ hipError_t launch_v(const NormArgs &a, hipStream_t st) {
 hipError_t launch_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride,
                              float scale, const float *residual, float *residual_out, const float *w_pre, float eps,
                              int64_t N, int64_t K, float *H, float *scales, int8_t *quants, hipStream_t st) {
-    NormArgs a;
-    a.block = block;
-    a.w_post = block ? w_post : nullptr;
-    a.gate = block ? gate : nullptr;
-    a.residual = residual;
-    a.w_pre = w_pre;
-    a.r_out = residual_out;
-    a.H = H;
-    a.scales = scales;
-    a.quants = quants;
-    a.N = N;
-    a.gate_stride = gate_stride;
-    a.K = (int)K;
-    a.scale = (double)scale;
-    a.eps = (double)eps;
-    return K % 4 == 0 ? launch_v<4>(a, st) : launch_v<1>(a, st);
+    // a grid holds fewer than 2^32 threads: at most 2^21 rows of 1024 per launch
+    constexpr int64_t kRows = int64_t(1) << 21;
+    for (int64_t n0 = 0; n0 < N; n0 += kRows) {
+        NormArgs a;
+        a.block = block ? block + n0 * K : nullptr;
+        a.w_post = block ? w_post : nullptr;
+        a.gate = block && gate ? gate + n0 * gate_stride : nullptr;
+        a.residual = residual + n0 * K;
+        a.w_pre = w_pre;
+        a.r_out = residual_out ? residual_out + n0 * K : nullptr;
+        a.H = H ? H + n0 * K : nullptr;
+        a.scales = scales ? scales + n0 * (K / 32) : nullptr;
+        a.quants = quants ? quants + n0 * K : nullptr;
+        a.N = N - n0 < kRows ? N - n0 : kRows;
+        a.gate_stride = gate_stride;
+        a.K = (int)K;
+        a.scale = (double)scale;
+        a.eps = (double)eps;
+        const hipError_t e = K % 4 == 0 ? launch_v<4>(a, st) : launch_v<1>(a, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace qmm

@@ -185,33 +185,39 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
 hipError_t launch_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, bool sigmoid, int64_t groups,
                             int64_t topk_groups, int group_top, int64_t topk, bool renorm, float scale, int32_t *ids,
                             float *weights, hipStream_t st) {
-    RouteArgs a;
-    a.logits = logits;
-    a.bias = bias;
-    a.ids = ids;
-    a.weights = weights;
-    a.N = N;
-    a.E = (int)E;
-    a.groups = (int)groups;
-    a.topk_groups = (int)topk_groups;
-    a.group_top = group_top;
-    a.topk = (int)topk;
-    a.sigmoid = sigmoid;
-    a.renorm = renorm;
-    a.scale = (double)scale;
     const int epl = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16;
-    // four tokens per workgroup while their scores stay below 64 KB of LDS
-    const unsigned wpb = epl > 4 ? 1 : (N >= 4 ? 4 : (unsigned)N);
-    const size_t lds = 8 * (size_t)wpb * (64 * epl + (groups > topk_groups ? 64 * epl + 2 * groups : 0));
-    const dim3 grid((unsigned)((N + wpb - 1) / wpb)), block(64 * wpb);
-    switch (epl) {
-    case 1: hipLaunchKernelGGL((route_kernel<1>), grid, block, lds, st, a); break;
-    case 2: hipLaunchKernelGGL((route_kernel<2>), grid, block, lds, st, a); break;
-    case 4: hipLaunchKernelGGL((route_kernel<4>), grid, block, lds, st, a); break;
-    case 8: hipLaunchKernelGGL((route_kernel<8>), grid, block, lds, st, a); break;
-    default: hipLaunchKernelGGL((route_kernel<16>), grid, block, lds, st, a); break;
+    // a grid holds fewer than 2^32 threads: at most 2^25 tokens per launch
+    constexpr int64_t kTokens = int64_t(1) << 25;
+    for (int64_t n0 = 0; n0 < N; n0 += kTokens) {
+        RouteArgs a;
+        a.logits = logits + n0 * E;
+        a.bias = bias;
+        a.ids = ids + n0 * topk;
+        a.weights = weights + n0 * topk;
+        a.N = N - n0 < kTokens ? N - n0 : kTokens;
+        a.E = (int)E;
+        a.groups = (int)groups;
+        a.topk_groups = (int)topk_groups;
+        a.group_top = group_top;
+        a.topk = (int)topk;
+        a.sigmoid = sigmoid;
+        a.renorm = renorm;
+        a.scale = (double)scale;
+        // four tokens per workgroup while their scores stay below 64 KB of LDS
+        const unsigned wpb = epl > 4 ? 1 : (a.N >= 4 ? 4 : (unsigned)a.N);
+        const size_t lds = 8 * (size_t)wpb * (64 * epl + (groups > topk_groups ? 64 * epl + 2 * groups : 0));
+        const dim3 grid((unsigned)((a.N + wpb - 1) / wpb)), block(64 * wpb);
+        switch (epl) {
+        case 1: hipLaunchKernelGGL((route_kernel<1>), grid, block, lds, st, a); break;
+        case 2: hipLaunchKernelGGL((route_kernel<2>), grid, block, lds, st, a); break;
+        case 4: hipLaunchKernelGGL((route_kernel<4>), grid, block, lds, st, a); break;
+        case 8: hipLaunchKernelGGL((route_kernel<8>), grid, block, lds, st, a); break;
+        default: hipLaunchKernelGGL((route_kernel<16>), grid, block, lds, st, a); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 }  // namespace qmm

@@ -411,8 +411,19 @@ int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, 
  *             (work_bytes; less is QMM_ERR_SCRATCH), 16-B aligned; NULL where
  *             that is 0.  Needs no initial value; clobbered.  Calls that overlap
  *             in time (two streams, two captured graphs) need separate work.
- * Both projections are f32 class for every N: with S the sum of |w x|
- * of a projection, |error| <= 1e-5 * S.  1 <= E <= QMM_MOE_MAX_EXPERTS,
+ * Few slots run the GEMV's f32 arithmetic, many the matrix cores (which form:
+ * the work bytes are 0 for the first).  Both are f32 class.  For a projection's
+ * sums, with S = sum |w x|:
+ *     few slots   |error| <= 1e-5 S
+ *     many slots  |error| <= 1e-5 Splus + 2^-29 max_k |x| sum_k |w|,
+ *                 Splus as for qmm_gemm_q8act (S, with the minima of Q4_1, Q4_K and
+ *                 Q5_K counted apart from the codes); the activations are split in
+ *                 two f16 parts under a power of two per row, so only a row whose
+ *                 values span more than 2^20 notices the second term.
+ * A non-finite activation makes that token's outputs non-finite (a matrix-core
+ * step also multiplies it by zero codes: NaN where the sum would be infinite)
+ * and no other token's.  Every slot's result is the same whatever other slots
+ * the call holds, as long as the form is the same.  1 <= E <= QMM_MOE_MAX_EXPERTS,
  * 1 <= T <= QMM_MOE_MAX_TOPK, N * T <= 2^31 - 1, M <= QMM_MOE_MAX_ROWS, K any
  * multiple of the block size up to QMM_MOE_MAX_K. */
 int64_t qmm_moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
@@ -427,7 +438,8 @@ int qmm_moe_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64
  *   H         device f32 [N][T][K], 16-B aligned (what qmm_moe_swiglu writes)
  *   residual  device f32 [N][M], 4-B aligned, or NULL: 0.  May be Y itself.
  *   Y         device f32 [N][M], 4-B aligned; overwritten
- *   ids, work, work_bytes and sizes as above, with qmm_moe_down_work_bytes
+ *   ids, work, work_bytes, sizes and the bound of each slot's product as above,
+ *   with qmm_moe_down_work_bytes
  * The slots are summed in a fixed order. */
 int64_t qmm_moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
 int qmm_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, const int32_t *ids,

@@ -167,3 +167,20 @@ def test_stream_and_graph_replays():
         call()
         torch.cuda.synchronize()
         assert torch.equal(got[0], r) and torch.equal(got[1], H), f"replay {i}"
+
+
+def test_more_rows_than_one_launch():
+    """2^21 rows go per launch: rows on both sides of the border, against f64 on the GPU."""
+    N, K = (1 << 21) + 3, 40
+    B, R = torch.randn(N, K, device="cuda"), torch.randn(N, K, device="cuda")
+    gt, w = torch.rand(N, K, device="cuda"), torch.rand(K, device="cuda")
+    r, H = torch.empty_like(R), torch.empty_like(R)
+    q.qmm_block_norm(R, N, K, residual_out=r, block=B, w_post=w, gate=gt, gate_stride=K, scale=0.5, w_pre=w, H=H)
+    torch.cuda.synchronize()
+    p = B.double()
+    p = 0.5 * gt.double() * p / torch.sqrt(p.square().mean(1, keepdim=True) + np.float64(np.float32(1e-5))) * w.double()
+    want = R.double() + p
+    assert torch.all((r.double() - want).abs() <= 2.0 ** -24 * want.abs() * (1 + 2.0 ** -20) + 1e-13 * (R.double().abs() + p.abs()))
+    h = r.double()
+    h = h / torch.sqrt(h.square().mean(1, keepdim=True) + np.float64(np.float32(1e-5))) * w.double()
+    assert torch.all((H.double() - h).abs() <= 2.0 ** -24 * h.abs() * (1 + 2.0 ** -20) + 1e-13 * h.abs())

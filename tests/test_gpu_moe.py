@@ -334,3 +334,73 @@ def test_block_together(N):
         block()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, outs)), f"replay {i}"
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_two_graphs_share_a_workspace_and_two_streams_do_not(many):
+    """Two captured calls with one workspace, replayed in turn on new inputs; then
+    two calls at once on two streams with a workspace each.  Bitwise against
+    calls by themselves."""
+    dt, E, M, K, T = q.QMM_Q5_K, 4, 130, 768, 2
+    N = tokens_on_matrix_cores(q.moe_down_work_bytes, dt, E, M, K, T) if many else 5
+    g = np.random.default_rng(4)
+    W = [dev(experts(dt, E, M, K, s)) for s in (0, 1)]
+    ids = [dev(g.integers(-1, E, (N, T), dtype=np.int32)) for _ in range(2)]
+    wt, H, R = (torch.randn(*s, device="cuda") for s in ((N, T), (N * T, K), (N, M)))
+    Y = [torch.empty(N, M, device="cuda") for _ in range(2)]
+    n = q.moe_down_work_bytes(dt, E, M, K, N, T)
+    assert (n > 0) == many
+    shared = work_of(n)
+    call = lambda i, out, work: q.qmm_moe_down(W[i], dt, E, M, K, N, T, ids[i], wt, H, out, residual=R, work=work)
+    call(0, Y[0], shared)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            call(i, Y[i], shared)
+    for rep in range(4):
+        H.normal_(), wt.normal_()
+        for i in (0, 1):
+            graphs[(i + rep) % 2].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            alone = torch.empty_like(Y[i])
+            call(i, alone, work_of(n))
+            torch.cuda.synchronize()
+            assert torch.equal(alone, Y[i]), f"replay {rep}, graph {i}"
+    streams, works = [torch.cuda.Stream() for _ in range(2)], [work_of(n) for _ in range(2)]
+    want = [y.clone() for y in Y]
+    torch.cuda.synchronize()
+    for rep in range(4):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                Y[i].zero_()
+                call(i, Y[i], works[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(Y, want)), f"round {rep}"
+
+
+def test_long_inputs_run_in_passes():
+    """More slots than one pass of the workspace holds (2^22 over T): rows on both sides of a pass's end."""
+    dt, E, M, K, T = q.QMM_Q4_0, 2, 3, 32, 2
+    N = (1 << 21) + 5
+    work = work_of(q.moe_down_work_bytes(dt, E, M, K, N, T))
+    assert work is not None and work.numel() < 2 * q.moe_down_work_bytes(dt, E, M, K, 1 << 21, T)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(-1, E, (N, T), device="cuda", dtype=torch.int32, generator=g)
+    H = torch.randn(N * T, K, device="cuda", generator=g)
+    wt = torch.randn(N, T, device="cuda", generator=g)
+    blob = experts(dt, E, M, K, 0)
+    Y = torch.full((N + 1, M), 7.0, device="cuda")
+    q.qmm_moe_down(dev(blob), dt, E, M, K, N, T, ids, wt, H, Y[:N], work=work)
+    torch.cuda.synchronize()
+    assert torch.all(Y[N] == 7.0)
+    W = torch.from_numpy(oracle.dequant(dt, blob, E * M, K)).cuda().view(E, M, K)
+    for lo, hi in ((0, 500), ((1 << 21) - 300, N)):
+        h, i, w = H.view(N, T, K)[lo:hi].double(), ids[lo:hi], wt[lo:hi].double()
+        Wi = torch.where((i >= 0)[..., None, None], W[i.clamp(min=0).long()], torch.zeros((), device="cuda", dtype=torch.float64))
+        y, S = (Wi * h[:, :, None]).sum(3), (Wi * h[:, :, None]).abs().sum(3)
+        want = (w[..., None] * y).sum(1)
+        tol = (w.abs()[..., None] * TAU * S).sum(1) + (T + 1) * 2.0 ** -24 * (w[..., None] * y).abs().sum(1)
+        assert torch.all((Y[lo:hi].double() - want).abs() <= tol)
