@@ -131,10 +131,10 @@ def lib():
         L.qmm_gemm_kernel.restype = ci
         L.qmm_read_probe.argtypes = [vp, i64, vp, vp]
         L.qmm_read_probe.restype = ci
-        f32 = ctypes.c_float
-        L.qmm_block_norm.argtypes = [vp, vp, vp, i64, f32, vp, vp, vp, f32, i64, i64, vp, vp, vp, vp]
+        f64 = ctypes.c_double
+        L.qmm_block_norm.argtypes = [vp, vp, vp, i64, f64, vp, vp, vp, f64, i64, i64, vp, vp, vp, vp]
         L.qmm_block_norm.restype = ci
-        L.qmm_moe_route.argtypes = [vp, vp, i64, i64, ci, i64, i64, ci, i64, ci, f32, vp, vp, vp]
+        L.qmm_moe_route.argtypes = [vp, vp, i64, i64, ci, i64, i64, ci, i64, ci, f64, vp, vp, vp]
         L.qmm_moe_route.restype = ci
         for f in (L.qmm_moe_swiglu_work_bytes, L.qmm_moe_down_work_bytes):
             f.argtypes = [ci, i64, i64, i64, i64, i64]

@@ -502,13 +502,13 @@ int qmm_gemm(const void *w_blob, int dtype, int64_t M, int64_t K, int64_t N, con
     return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 
-int qmm_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride, float scale,
-                   const float *residual, float *residual_out, const float *w_pre, float eps, int64_t N, int64_t K,
+int qmm_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride, double scale,
+                   const float *residual, float *residual_out, const float *w_pre, double eps, int64_t N, int64_t K,
                    float *H, float *scales, int8_t *quants, void *stream) {
     if (N < 1 || N > INT32_MAX || K < 1 || K > (int64_t(1) << 28)) return QMM_ERR_SHAPE;
     if (block && gate && gate_stride != 0 && gate_stride != K) return QMM_ERR_SHAPE;
     if (quants && K % 32 != 0) return QMM_ERR_SHAPE;
-    if (!std::isfinite(scale) || !std::isfinite(eps) || eps < 0.f) return QMM_ERR_VALUE;
+    if (!std::isfinite(scale) || !std::isfinite(eps) || eps < 0.0) return QMM_ERR_VALUE;
     if (!residual || (block && !residual_out) || (!scales != !quants)) return QMM_ERR_NULL;
     if (!residual_out && !H && !quants) return QMM_ERR_NULL;  // nothing to write
     for (const void *p : {(const void *)block, (const void *)w_post, (const void *)gate, (const void *)residual,
@@ -524,7 +524,7 @@ int qmm_block_norm(const float *block, const float *w_post, const float *gate, i
 }
 
 int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, int scoring, int64_t groups,
-                  int64_t topk_groups, int group_top, int64_t topk, int renorm, float scale, int32_t *ids,
+                  int64_t topk_groups, int group_top, int64_t topk, int renorm, double scale, int32_t *ids,
                   float *weights, void *stream) {
     if (N < 1 || N > INT32_MAX || E < 1 || E > QMM_MOE_MAX_EXPERTS) return QMM_ERR_SHAPE;
     if (groups < 1 || groups > E || E % groups != 0 || topk_groups < 1 || topk_groups > groups) return QMM_ERR_SHAPE;

@@ -110,12 +110,12 @@ hipError_t launch_gemv_q8in(int mode, int n, const void *const *blobs, const int
 // (qmm_norm.hip): K <= 2^28, block / w_post / gate / residual_out / w_pre / H /
 // (scales, quants) may be NULL as qmm_block_norm allows.
 hipError_t launch_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride,
-                             float scale, const float *residual, float *residual_out, const float *w_pre, float eps,
+                             double scale, const float *residual, float *residual_out, const float *w_pre, double eps,
                              int64_t N, int64_t K, float *H, float *scales, int8_t *quants, hipStream_t st);
 
 // Routing (qmm_route.hip): E <= QMM_MOE_MAX_EXPERTS, topk <= QMM_MOE_MAX_TOPK.
 hipError_t launch_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, bool sigmoid, int64_t groups,
-                            int64_t topk_groups, int group_top, int64_t topk, bool renorm, float scale, int32_t *ids,
+                            int64_t topk_groups, int group_top, int64_t topk, bool renorm, double scale, int32_t *ids,
                             float *weights, hipStream_t st);
 
 // The routed experts' products (qmm_moe.hip).  `work` holds the work bytes of

@@ -288,7 +288,7 @@ hipError_t launch_v(const NormArgs &a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride,
-                             float scale, const float *residual, float *residual_out, const float *w_pre, float eps,
+                             double scale, const float *residual, float *residual_out, const float *w_pre, double eps,
                              int64_t N, int64_t K, float *H, float *scales, int8_t *quants, hipStream_t st) {
     // a grid holds fewer than 2^32 threads: at most 2^21 rows of 1024 per launch
     constexpr int64_t kRows = int64_t(1) << 21;
@@ -306,8 +306,8 @@ hipError_t launch_block_norm(const float *block, const float *w_post, const floa
         a.N = N - n0 < kRows ? N - n0 : kRows;
         a.gate_stride = gate_stride;
         a.K = (int)K;
-        a.scale = (double)scale;
-        a.eps = (double)eps;
+        a.scale = scale;
+        a.eps = eps;
         const hipError_t e = K % 4 == 0 ? launch_v<4>(a, st) : launch_v<1>(a, st);
         if (e != hipSuccess) return e;
     }

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
 }  // namespace
 
 hipError_t launch_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, bool sigmoid, int64_t groups,
-                            int64_t topk_groups, int group_top, int64_t topk, bool renorm, float scale, int32_t *ids,
+                            int64_t topk_groups, int group_top, int64_t topk, bool renorm, double scale, int32_t *ids,
                             float *weights, hipStream_t st) {
     const int epl = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16;
     // a grid holds fewer than 2^32 threads: at most 2^25 tokens per launch
@@ -202,7 +202,7 @@ hipError_t launch_moe_route(const float *logits, const float *bias, int64_t N, i
         a.topk = (int)topk;
         a.sigmoid = sigmoid;
         a.renorm = renorm;
-        a.scale = (double)scale;
+        a.scale = scale;
         // four tokens per workgroup while their scores stay below 64 KB of LDS
         const unsigned wpb = epl > 4 ? 1 : (a.N >= 4 ? 4 : (unsigned)a.N);
         const size_t lds = 8 * (size_t)wpb * (64 * epl + (groups > topk_groups ? 64 * epl + 2 * groups : 0));

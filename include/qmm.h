@@ -340,7 +340,7 @@ int qmm_gemm_repacked_kernel(int dtype, int64_t M, int64_t K, int64_t N);
  *     p = block[n], or, with w_post, block[n] / sqrt(mean(block[n]^2) + eps) * w_post
  *     r = residual[n] + scale * gate * p        -> residual_out[n]
  *     h = r / sqrt(mean(r^2) + eps) * w_pre     -> H[n], and/or its Q8_0 blocks
- * Computed in f64; r and h are rounded to f32 once, and h is computed from the
+ * Computed in f64 (scale and eps too); r and h are rounded to f32 once, and h is computed from the
  * rounded r.  The Q8_0 blocks are those qmm_quantize_q8_0 makes of the f32 h
  * (the bits it writes), ready for qmm_gemm_q8act.
  *   block        device f32 [N][K], or NULL: r = residual (a plain norm)
@@ -360,8 +360,8 @@ int qmm_gemm_repacked_kernel(int dtype, int64_t M, int64_t K, int64_t N);
  * gate without a block are ignored.  Apart from residual_out == residual the
  * outputs overlap nothing.  1 <= N <= 2^31 - 1, 1 <= K <= 2^28; every pointer
  * 16-B aligned. */
-int qmm_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride, float scale,
-                   const float *residual, float *residual_out, const float *w_pre, float eps, int64_t N, int64_t K,
+int qmm_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride, double scale,
+                   const float *residual, float *residual_out, const float *w_pre, double eps, int64_t N, int64_t K,
                    float *H, float *scales, int8_t *quants, void *stream);
 
 /* Routing of N tokens to topk of E experts each.  Per token, in f64:
@@ -393,7 +393,7 @@ int qmm_block_norm(const float *block, const float *w_post, const float *gate, i
 #define QMM_MOE_MAX_ROWS 4194304
 #define QMM_MOE_MAX_K 1048576
 int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, int scoring, int64_t groups,
-                  int64_t topk_groups, int group_top, int64_t topk, int renorm, float scale, int32_t *ids,
+                  int64_t topk_groups, int group_top, int64_t topk, int renorm, double scale, int32_t *ids,
                   float *weights, void *stream);
 
 /* The routed experts' gate/up projections with SwiGLU.  Token n has T slots;

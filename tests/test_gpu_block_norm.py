@@ -66,7 +66,7 @@ def check(N, K, post=True, gate="row", pre=True, block=True, h=True, q8=False, s
     want, terms = R.astype(np.float64), np.abs(R.astype(np.float64))
     if block:
         p = unit(B.astype(np.float64), wp, eps) if post else B.astype(np.float64)
-        p = np.float64(np.float32(scale)) * p * (1.0 if gt is None else gt.astype(np.float64))
+        p = scale * p * (1.0 if gt is None else gt.astype(np.float64))
         want, terms = want + p, terms + np.abs(p)
         close(r, want, terms)
         rk = r.cpu().numpy()
@@ -124,6 +124,7 @@ def test_large_and_small_values():
     check(4, 4096, mag=1e-30, eps=0.0)
     check(4, 257, mag=1e19, q8=False)
     check(300, 4096, seed=3)
+    check(64, 4096, seed=5, scale=0.22, q8=True)  # a scale that f32 does not hold
     check(1025, 40, seed=4)
 
 
@@ -178,9 +179,9 @@ def test_more_rows_than_one_launch():
     q.qmm_block_norm(R, N, K, residual_out=r, block=B, w_post=w, gate=gt, gate_stride=K, scale=0.5, w_pre=w, H=H)
     torch.cuda.synchronize()
     p = B.double()
-    p = 0.5 * gt.double() * p / torch.sqrt(p.square().mean(1, keepdim=True) + np.float64(np.float32(1e-5))) * w.double()
+    p = 0.5 * gt.double() * p / torch.sqrt(p.square().mean(1, keepdim=True) + 1e-5) * w.double()
     want = R.double() + p
     assert torch.all((r.double() - want).abs() <= 2.0 ** -24 * want.abs() * (1 + 2.0 ** -20) + 1e-13 * (R.double().abs() + p.abs()))
     h = r.double()
-    h = h / torch.sqrt(h.square().mean(1, keepdim=True) + np.float64(np.float32(1e-5))) * w.double()
+    h = h / torch.sqrt(h.square().mean(1, keepdim=True) + 1e-5) * w.double()
     assert torch.all((H.double() - h).abs() <= 2.0 ** -24 * h.abs() * (1 + 2.0 ** -20) + 1e-13 * h.abs())

@@ -50,7 +50,7 @@ def reference(logits, bias, k, scoring, groups, keep, top, renorm, scale):
         if renorm:
             t = math.fsum(w)
             w = [v / t if t > 0 else 0.0 for v in w]
-        ids[n], ws[n] = pick, [v * float(np.float32(scale)) for v in w]
+        ids[n], ws[n] = pick, [v * scale for v in w]
     return ids, ws
 
 
