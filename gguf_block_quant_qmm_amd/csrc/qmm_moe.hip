@@ -76,12 +76,11 @@ struct MoeGemvArgs {
 
 // One workgroup: `rows` rows of one slot's expert (SWI), or of every expert of
 // one token.  W wavefronts; items round by round when there are more.
-// ODD: an odd number of 32-weight blocks per row.
+// ODD: an odd number of 32-weight blocks per row.  Two wavefronts per SIMD:
+// registers for three spill the activations (gate/up of one token, 8 experts of
+// 14336 x 4096 Q4_0, 2 each: 31 us with two, 43 with three).
 template <int DT, bool SWI, int LPR, bool ODD>
-#ifndef GV_OCC
-#define GV_OCC 2
-#endif
-__global__ void __launch_bounds__(512, GV_OCC) moe_gemv_kernel(const MoeGemvArgs a) {
+__global__ void __launch_bounds__(512, 2) moe_gemv_kernel(const MoeGemvArgs a) {
     constexpr int RPW = 64 / LPR, NL = Unit<DT>::NL, NM = SWI ? 2 : 1;
     constexpr int D = 3 * NM * NL <= 60 ? 2 : 1;  // row groups in flight behind the current one
     extern __shared__ __attribute__((aligned(16))) floatx4 xs[];
@@ -244,11 +243,11 @@ hipError_t run_gemv(const void *w0, const void *w1, int64_t E, int64_t M, int64_
     a.phases = items == 1 ? 4 : std::max(1, 8 / per_round);
     const int W = per_round * a.phases, rpw = 64 / lpr;
     const int64_t jobs = SWI ? N * T : N;
-    // rows per workgroup: about 16 wavefronts per CU (8 where every wavefront
-    // stages activations of its own), whole row groups for every phase
-    static const int wpc_lever = tuning_lever("QMM_MOE_GEMV_WPC", 0);
-    const int wpc = wpc_lever ? wpc_lever : (items == 1 ? 16 : 8);
-    const int64_t wgs = std::max<int64_t>(1, (int64_t)cus * wpc / W);
+    // rows per workgroup: 8 wavefronts per CU, as many as run at a time, so that
+    // each stages its activations once; whole row groups for every phase.  Against
+    // 16 per CU: gate/up of one token, 2 experts of 14336 x 4096 Q4_0, 30.7 against
+    // 33.4 us; 8 of 1024 x 2048 Q4_K, 8.7 against 9.8
+    const int64_t wgs = std::max<int64_t>(1, (int64_t)cus * 8 / W);
     const int64_t step = (int64_t)rpw * a.phases;
     const int64_t tiles_max = std::max<int64_t>(1, wgs / jobs);  // no last, nearly empty round of workgroups
     int64_t rows = (M + tiles_max - 1) / tiles_max;

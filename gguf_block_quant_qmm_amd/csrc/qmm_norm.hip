@@ -12,7 +12,9 @@
 // vanish in f64.  h is computed from the rounded r, the value that
 // residual_out holds and the next block adds to.
 //
-// One read of the inputs and one write of the outputs: a row of up to 16384
+// Memory-bound: 4096 rows of 4096 (block, residual in; r, h out) take 52 us, 5.2
+// TB/s, the rate of a large copy on this card (5.1).  One read of the inputs and
+// one write of the outputs: a row of up to 16384
 // values lives in registers (a wavefront per row up to 1024 values, else a
 // workgroup), the two sums of squares are wavefront reductions with DPP moves
 // joined over the workgroup through LDS in wavefront order.  Longer rows are
@@ -270,11 +272,13 @@ hipError_t launch_v(const NormArgs &a, hipStream_t st) {
         else if (nv <= 128) hipLaunchKernelGGL((norm_kernel<V, 2, true>), grid, block, 0, st, a);
         else hipLaunchKernelGGL((norm_kernel<V, 4, true>), grid, block, 0, st, a);
     } else if (nv <= (V == 4 ? 4096 : 16384)) {
-        const int per = nv <= 1024 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : nv <= 8192 ? 8 : 16;
+        // few wavefronts with many loads each.  4096 x 4096: 256 threads a row
+        // (4 vectors each) 52 us, 512 54, 1024 67.5, 128 92; one row: 3.9, 4.6, 4.8,
+        // 7.1 us.  Odd widths: 37 x 4099 with 8 values a thread 5.2 us, 16 5.6
+        const int64_t per = V == 4 ? (nv <= 512 ? 2 : 4) : (nv <= 1024 ? 4 : nv <= 4608 ? 8 : 16);
         const dim3 grid((unsigned)a.N), block((unsigned)(((nv + per - 1) / per + 63) / 64 * 64));
         switch (per) {
-        case 1: hipLaunchKernelGGL((norm_kernel<V, 1, false>), grid, block, 0, st, a); break;
-        case 2: hipLaunchKernelGGL((norm_kernel<V, 2, false>), grid, block, 0, st, a); break;
+        case 2: if constexpr (V == 4) hipLaunchKernelGGL((norm_kernel<V, 2, false>), grid, block, 0, st, a); break;
         case 4: hipLaunchKernelGGL((norm_kernel<V, 4, false>), grid, block, 0, st, a); break;
         case 8: if constexpr (V == 1) hipLaunchKernelGGL((norm_kernel<V, 8, false>), grid, block, 0, st, a); break;
         default: if constexpr (V == 1) hipLaunchKernelGGL((norm_kernel<V, 16, false>), grid, block, 0, st, a); break;
