@@ -130,7 +130,6 @@ hipError_t launch_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64
                            void *work, hipStream_t st, int cus);
 
 // The matrix-core form of both (qmm_moe_gemm.hip).
-int moe_gemm_bn(int64_t E, int64_t N, int64_t T);  // slots per tile
 int64_t moe_gemm_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, bool down);
 hipError_t launch_moe_gemm_swiglu(const void *gate, const void *up, int dtype, int64_t E, int64_t M, int64_t K, int64_t N,
                                   int64_t T, const int32_t *ids, const float *X, float *out, void *work, hipStream_t st);

@@ -527,41 +527,25 @@ struct MoeGemmArgs {
     uint32_t xs_bytes;       // of ws.xs
 };
 
-// A workgroup: W wavefronts, each 2 x 32 rows (swiglu: 32 gate rows and the
-// same 32 up rows) against the BN = 32 FN slots of a tile.  Weights: a
-// wavefront loads its own rows' bytes of a k-tile in runs of 64 or 128 bytes
-// (lanes reading a row each would touch 32 cache lines per instruction), parks
-// them in its part of LDS one k-tile ahead and reads each lane's bytes from
-// there.  Activations: all wavefronts share the tile's rows, double-buffered.
-template <int DT, int FN, int W, bool SWI>
-__global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a) {
+// k-tiles [k0, k1) of one job: W wavefronts, each 2 x 32 rows of the matrix
+// (swiglu: 32 gate rows and the same 32 up rows) against the n_rows <= 32 FN
+// slots of a tile.  Weights: a wavefront loads its own rows' bytes of a k-tile in
+// runs of 64 or 128 bytes (lanes reading a row each would touch 32 cache lines
+// per instruction), parks them in its part of LDS one k-tile ahead and reads each
+// lane's bytes from there.  Activations: all wavefronts share the tile's rows,
+// double-buffered.
+template <int DT, int FN, int BN, int W, bool SWI>
+__device__ __forceinline__ void moe_tile(const MoeGemmArgs &a, const int4 tile, int e, int n_rows, int mt, int split, int k0, int k1,
+                                         uint8_t (*xl)[BN * XT_BYTES], uint8_t (*wl)[64 * MDec<DT>::ROW], int32_t *slot_of,
+                                         float *rsc) {
     using D = MDec<DT>;
-    constexpr int BN = 32 * FN, RW = SWI ? 32 : 64, BM = RW * W;
-    constexpr int NP = BN * 16 / (64 * W);  // 16-byte pieces of half a k-tile per thread
+    constexpr int FR = 32 * FN, RW = SWI ? 32 : 64, BM = RW * W;
+    constexpr int NP = FR * 16 / (64 * W);  // 16-byte pieces of half a k-tile per thread
     static_assert(NP >= 1, "tile too small for the workgroup");
     constexpr int RI = 64 / D::LP, MI = 64 / RI;  // rows per main load instruction, instructions per k-tile
-    __shared__ __attribute__((aligned(16))) uint8_t xl[2][BN * XT_BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t wl[W][64 * D::ROW];
-    __shared__ int32_t slot_of[BN];
-    __shared__ float rsc[BN];
     const int t = (int)threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l32 = lane & 31, kh = lane >> 5;
-
-    // An XCD (workgroup id mod 8) takes a run of jobs, ordered by expert, then
-    // rows of its matrix, then its tiles of slots: the workgroups running on it
-    // at a time share one expert's slots (a few MB, its L2) and read the same
-    // rows together
-    const int per_tile = a.mtiles * a.splits;
-    const int nt = a.ws.tiles[0].x, total = nt * per_tile, chunk = (total + 7) / 8;
-    const int id = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
-    if (((int)blockIdx.x >> 3) >= chunk || id >= total) return;
-    const int4 of_job = a.ws.tiles[1 + id / per_tile];  // some tile of the job's expert
-    const int t0 = of_job.w, tc = of_job.z >> 8, r_id = id - t0 * per_tile;
-    const int mt = r_id / tc / a.splits, split = r_id / tc % a.splits;
-    const int k0 = split * a.kper, k1 = k0 + a.kper < a.nkt ? k0 + a.kper : a.nkt;  // k-tiles [k0, k1)
-    const int4 tile = a.ws.tiles[1 + t0 + r_id % tc];
-    const int e = __builtin_amdgcn_readfirstlane(tile.x), n_rows = __builtin_amdgcn_readfirstlane(tile.z & 0xFF);
-    for (int i = t; i < BN; i += 64 * W) {
+    for (int i = t; i < FR; i += 64 * W) {
         const int s = i < n_rows ? a.ws.order[tile.y + i] : -1;
         slot_of[i] = s;
         rsc[i] = s >= 0 ? a.ws.rscale[s / a.T] : 0.f;
@@ -812,6 +796,35 @@ __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a
         }
 }
 
+// One workgroup per job.  A tile of 64 that holds up to 32 slots, often an
+// expert's last one, runs half of the matrix steps (down of 2 of 8 experts 4096 x
+// 14336 Q6_K, 512 tokens: 685 us against 728 with every tile run in full; of 8 of
+// 64 experts 4096 x 1024 Q8_0: 187 against 195).
+template <int DT, int FN, int W, bool SWI>
+__global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a) {
+    constexpr int BN = 32 * FN;
+    __shared__ __attribute__((aligned(16))) uint8_t xl[2][BN * XT_BYTES];           // two half k-tiles of activations
+    __shared__ __attribute__((aligned(16))) uint8_t wl[W][64 * MDec<DT>::ROW];      // each wavefront's rows
+    __shared__ int32_t slot_of[BN];
+    __shared__ float rsc[BN];
+    // An XCD (workgroup id mod 8) takes a run of jobs, ordered by expert, then
+    // rows of its matrix, then its tiles of slots: the workgroups running on it
+    // at a time share one expert's slots (a few MB, its L2) and read the same
+    // rows together
+    const int per_tile = a.mtiles * a.splits;
+    const int nt = a.ws.tiles[0].x, total = nt * per_tile, chunk = (total + 7) / 8;
+    const int id = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
+    if (((int)blockIdx.x >> 3) >= chunk || id >= total) return;
+    const int4 of_job = a.ws.tiles[1 + id / per_tile];  // some tile of the job's expert
+    const int t0 = of_job.w, tc = of_job.z >> 8, r_id = id - t0 * per_tile;
+    const int mt = r_id / tc / a.splits, split = r_id / tc % a.splits;
+    const int k0 = split * a.kper, k1 = k0 + a.kper < a.nkt ? k0 + a.kper : a.nkt;  // k-tiles [k0, k1)
+    const int4 tile = a.ws.tiles[1 + t0 + r_id % tc];
+    const int e = __builtin_amdgcn_readfirstlane(tile.x), n_rows = __builtin_amdgcn_readfirstlane(tile.z & 0xFF);
+    if (FN == 1 || n_rows > 32) moe_tile<DT, FN, BN, W, SWI>(a, tile, e, n_rows, mt, split, k0, k1, xl, wl, slot_of, rsc);
+    else moe_tile<DT, 1, BN, W, SWI>(a, tile, e, n_rows, mt, split, k0, k1, xl, wl, slot_of, rsc);
+}
+
 // Y[n][m] = residual[n][m] + sum over t of weights[n][t] * prod[n T + t][m], t
 // ascending, a slot's product the sum of its splits' parts.  V values per thread (4: M % 4 == 0 and 16-byte aligned rows).
 // Four slots' rows are in flight at once; a slot without an expert is an empty
@@ -896,6 +909,15 @@ int64_t chunk_tokens(int64_t E, int64_t K, int64_t M, int64_t N, int64_t T, bool
 }
 
 constexpr int GEMM_W = 4;  // wavefronts per workgroup
+
+// Slots per tile: 32 while an expert sees few of them, else 64 (half the weight
+// reads and decoding per slot, but fewer and fuller workgroups).  64 experts, 8
+// each, gate/up 1024 x 2048 Q4_K, tiles of 32 against 64: 200 tokens 83 against
+// 102 us, 400 tokens (50 slots each) 114 against 125, 1000 tokens 209 against 200;
+// down 2048 x 1024 Q8_0: 200 tokens 76 against 84, 400 tokens 101 against 95; 8
+// experts, 2 each, 14336 x 4096 Q4_K: 192 tokens (48 slots) 325 against 344, 256
+// tokens 410 against 395.
+int moe_gemm_bn(int64_t E, int64_t N, int64_t T) { return N * T <= 48 * E ? 32 : 64; }
 
 struct MoeSizes {
     int64_t tokens, slots, rows, nkt, tiles, mtiles, splits, kper;
@@ -992,9 +1014,6 @@ hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_
 }
 
 }  // namespace
-
-// Slots per tile: 32 while an expert sees few of them, else 64.
-int moe_gemm_bn(int64_t E, int64_t N, int64_t T) { return N * T <= 32 * E ? 32 : 64; }
 
 int64_t moe_gemm_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, bool down) {
     return moe_sizes(dtype, E, M, K, N, T, moe_gemm_bn(E, N, T), down).bytes;
