@@ -4,6 +4,10 @@
 //
 // Few tokens: the GEMV's f32 arithmetic (qmm_units.hpp), memory-bound on the
 // chosen experts' bytes.  Many tokens: the matrix cores (qmm_moe_gemm.hip).
+// Measured, gate/up of 1 token, 2 of 8 experts 14336 x 4096: Q4_0 25 us (5.2 TB/s),
+// Q8_0 48 us (5.2), Q6_K 41 us (4.7); down of 2 of 8 experts 4096 x 14336 Q6_K
+// 22 us (4.3).  The K-quants' decoding costs more than the reads wait: down of 7
+// tokens, 8 of 64 experts 4096 x 1024 Q5_K, 38 us (4.2 TB/s), 28 of them VALU issue.
 //
 // The few-token kernel cuts a row into units of 64 weights, one per lane, as
 // the GEMV does, but an expert's rows are often short (K of a few hundred

@@ -11,6 +11,10 @@
 // running choices are f64 values with NaN for an expert that is out (chosen, or
 // in a closed group): v_max_f64 passes over NaN, so a maximum over the
 // wavefront is two DPP moves and one instruction per step.
+//
+// Bound by the chain of topk maxima, each waiting for the one before it: 1 token,
+// 8 of 64 experts, 3.3 us; 4096 tokens, 256 experts in groups, 10-11 us (4 MB of
+// logits: 1 us of memory time).
 #include "qmm_device.hpp"
 #include "qmm_internal.hpp"
 

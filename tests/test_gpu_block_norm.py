@@ -128,6 +128,19 @@ def test_large_and_small_values():
     check(1025, 40, seed=4)
 
 
+@pytest.mark.parametrize("K", [96, 4096, 20000])
+def test_scale_and_norm_beyond_f64_together(K):
+    """A scale of 1e300 on a block of 1e-30: scale / norm is beyond f64, the products with the block's zeros are 0."""
+    B = np.full((2, K), 1e-30, np.float32)
+    B[:, ::3] = 0.0
+    R = np.random.default_rng(9).standard_normal((2, K)).astype(np.float32)
+    for scale, want in ((1e300, np.where(B == 0.0, R, np.float32(np.inf))), (-1e300, np.where(B == 0.0, R, np.float32(-np.inf)))):
+        r = torch.empty((2, K), device="cuda")
+        q.qmm_block_norm(dev(R), 2, K, residual_out=r, block=dev(B), w_post=dev(np.ones(K, np.float32)), scale=scale, eps=0.0)
+        torch.cuda.synchronize()
+        assert np.array_equal(r.cpu().numpy(), want)
+
+
 def test_zero_rows_and_non_finite_values_stay_in_their_row():
     N, K = 5, 4096
     R = np.random.default_rng(3).standard_normal((N, K)).astype(np.float32)
