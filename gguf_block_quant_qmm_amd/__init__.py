@@ -441,7 +441,9 @@ def _work(work) -> tuple[int, int]:
     """Address and bytes of a work tensor (None or an empty one: no work)."""
     if work is None:
         return 0, 0
-    return _addr(work, None, "work"), work.numel() * work.element_size()
+    if isinstance(work, int):
+        raise ValueError("work must be a device tensor (an address alone has no size)")
+    return _addr(work, None, "work"), work.nbytes
 
 
 def qmm_moe_swiglu(gate, up, dtype: int, E: int, M: int, K: int, N: int, T: int, ids, X, out, work=None,

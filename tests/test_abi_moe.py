@@ -128,3 +128,9 @@ def test_valid_calls_without_gpu_report_device():
 
 def test_strerror_names_the_value_status():
     assert "range" in q.strerror(q.QMM_ERR_VALUE) and ctypes.c_char_p(q.strerror(-7).encode()).value
+
+
+def test_work_without_a_size_is_refused():
+    for call, rest in ((q.qmm_moe_swiglu, (A, A, 2, 8, 64, 256, 64, 2, A, A, A)), (q.qmm_moe_down, (A, 2, 8, 64, 256, 64, 2, A, A, A, A))):
+        with pytest.raises(ValueError, match="work"):
+            call(*rest, work=A)
