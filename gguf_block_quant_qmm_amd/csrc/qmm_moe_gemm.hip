@@ -439,12 +439,13 @@ __device__ __forceinline__ void put_piece(const MoeWs &ws, int64_t row, int nkt,
 }
 
 // Workgroup 0 plans the tiles; the others split rows, WPR of their 4 wavefronts
-// on each.  REG: a row (K <= 1024 WPR) stays in registers between its maximum
-// and the split; else it is read twice.  zero_out (gate/up): the output rows [M]
+// on each.  PPL > 0: a row (K <= 512 WPR PPL) stays in registers between its
+// maximum and the split, PPL pieces per lane; else it is read twice (1024 rows of
+// 14336: 27 us read twice, 22.6 in registers).  zero_out (gate/up): the output rows [M]
 // of a token's slots without an expert are cleared here, for the GEMM writes
 // only rows that have one.  slot_rows (down): rows are slots, and those without
 // an expert are skipped.
-template <int DT, int WPR, bool REG>
+template <int DT, int WPR, int PPL>
 __global__ void __launch_bounds__(256) moe_prep_kernel(const int32_t *ids, int S, int E, int BN, MoeWs ws, const float *X,
                                                        int64_t rows, int K, int nkt, int T, bool slot_rows, float *zero_out,
                                                        int64_t M) {
@@ -483,9 +484,8 @@ __global__ void __launch_bounds__(256) moe_prep_kernel(const int32_t *ids, int S
         a = __builtin_bit_cast(floatx4, ld128(rs, k, 0));
         b = __builtin_bit_cast(floatx4, ld128(rs, k + 16u, 0));
     };
-    constexpr int PPL = 2;
-    floatx4 va[PPL], vb[PPL];
-    if constexpr (REG) {
+    floatx4 va[PPL > 0 ? PPL : 1], vb[PPL > 0 ? PPL : 1];
+    if constexpr (PPL > 0) {
 #pragma unroll
         for (int j = 0; j < PPL; j++) load(t + TPR * j, va[j], vb[j]);
 #pragma unroll
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(256) moe_prep_kernel(const int32_t *ids, int S
     m = m > 126 ? 126 : m;
     const float mul = ldexpf(1.0f, m);
     if (t == 0) ws.rscale[row] = ldexpf(1.0f, -m);
-    if constexpr (REG) {
+    if constexpr (PPL > 0) {
 #pragma unroll
         for (int j = 0; j < PPL; j++)
             if (t + TPR * j < n) put_piece<DT>(ws, row, nkt, t + TPR * j, va[j], vb[j], mul);
@@ -995,13 +995,15 @@ hipError_t run_gemm(const void *w0, const void *w1, int64_t E, int64_t M, int64_
         const float *xc = X + n0 * (SWI ? 1 : T) * K;
         const int wpr = K <= 1024 ? 1 : K <= 2048 ? 2 : 4;  // wavefronts per row
         const dim3 pg((unsigned)((rows * wpr + 3) / 4 + 1));
-#define QMM_PREP(WPR, REG)                                                                                              \
-    hipLaunchKernelGGL((moe_prep_kernel<DT, WPR, REG>), pg, dim3(256), 0, st, idc, (int)S, (int)E, BN, a.ws, xc, rows, (int)K, \
+#define QMM_PREP(WPR, PPL)                                                                                              \
+    hipLaunchKernelGGL((moe_prep_kernel<DT, WPR, PPL>), pg, dim3(256), 0, st, idc, (int)S, (int)E, BN, a.ws, xc, rows, (int)K, \
                        (int)z.nkt, (int)T, !SWI, a.out, M)
-        if (wpr == 1) QMM_PREP(1, true);
-        else if (wpr == 2) QMM_PREP(2, true);
-        else if (K <= 4096) QMM_PREP(4, true);
-        else QMM_PREP(4, false);
+        if (wpr == 1) QMM_PREP(1, 2);
+        else if (wpr == 2) QMM_PREP(2, 2);
+        else if (K <= 4096) QMM_PREP(4, 2);
+        else if (K <= 8192) QMM_PREP(4, 4);
+        else if (K <= 16384) QMM_PREP(4, 8);
+        else QMM_PREP(4, 0);
 #undef QMM_PREP
         const int64_t tiles = S / BN + std::min(E, S);
         if (BN == 32) launch_gemm<DT, 1, W, SWI>(a, tiles, st);

@@ -27,6 +27,12 @@ Subcommands (run from the repository root):
            that every launch reads its weights from HBM): the program the
            per-shape counter runs profile.
 
+  moe      --dtype Q4_K --E 8 --M 14336 --K 4096 --N 512 --T 2 --reps R
+           Runs one sparse feed-forward block R times: qmm_block_norm over N
+           rows of K, qmm_moe_route to T of E experts, qmm_moe_swiglu (M x K)
+           and qmm_moe_down (K x M) with the residual; random blobs of one
+           dtype, enough copies of the three expert tensors to fill 1 GiB.
+
   counters --csv <counter_collection.csv> --key REGEX --title T --cmd C
            Markdown table of every counter in a --pmc run, the mean per
            dispatch (summed over the device) of the dispatches whose kernel
@@ -98,6 +104,37 @@ def _gemm(args):
     torch.cuda.synchronize()
     print(f"qmm_gemm {args.dtype} {args.M}x{args.K} N={args.N} x {args.reps} (kernel id "
           f"{q.gemm_kernel(dt, args.M, args.K, args.N)}, {len(copies)} copies)", flush=True)
+
+
+def _moe(args):
+    import torch
+
+    import gguf_block_quant_qmm_amd as q
+    from qmm_inputs import BY_NAME, make_blob, rng_for
+    dt, E, M, K, N, T = BY_NAME[args.dtype], args.E, args.M, args.K, args.N, args.T
+
+    def experts(rows, k, seed):
+        one = torch.from_numpy(make_blob(dt, rows, k, rng_for(91, seed))).cuda()
+        return one.repeat(E)  # E experts of the same weights: distinct bytes in memory
+
+    sets = [[experts(M, K, 0), experts(M, K, 1), experts(K, M, 2)]]
+    while sum(t.numel() for s in sets for t in s) < 1 << 30:
+        sets.append([t.clone() for t in sets[0]])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    randn = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    x, block, logits, w = randn(N, K), randn(N, K), 1.5 * randn(N, E) + 0.5 * randn(E), 1 + 0.1 * randn(K)
+    h, act, y = torch.empty_like(x), torch.empty((N, T, M), device="cuda"), torch.empty_like(x)
+    ids, wt = torch.empty((N, T), dtype=torch.int32, device="cuda"), torch.empty((N, T), device="cuda")
+    nb = max(q.moe_swiglu_work_bytes(dt, E, M, K, N, T), q.moe_down_work_bytes(dt, E, K, M, N, T))
+    work = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    for r in range(args.reps):
+        gate, up, down = sets[r % len(sets)]
+        q.qmm_block_norm(x, N, K, residual_out=y, block=block, w_post=w, w_pre=w, H=h)
+        q.qmm_moe_route(logits, N, E, T, ids, wt)
+        q.qmm_moe_swiglu(gate, up, dt, E, M, K, N, T, ids, h, act, work=work)
+        q.qmm_moe_down(down, dt, E, K, M, N, T, ids, wt, act, y, residual=y, work=work)
+    torch.cuda.synchronize()
+    print(f"sparse block {args.dtype} E={E} {M}x{K} N={N} T={T} x {args.reps} (work {nb} bytes, {len(sets)} copies)", flush=True)
 
 
 def _counters(args):
@@ -356,6 +393,14 @@ def main(argv=None):
     g.add_argument("--K", type=int, default=4096)
     g.add_argument("--N", type=int, default=32)
     g.add_argument("--reps", type=int, default=20)
+    o = sub.add_parser("moe")
+    o.add_argument("--dtype", default="Q4_K")
+    o.add_argument("--E", type=int, default=8)
+    o.add_argument("--M", type=int, default=14336)
+    o.add_argument("--K", type=int, default=4096)
+    o.add_argument("--N", type=int, default=512)
+    o.add_argument("--T", type=int, default=2)
+    o.add_argument("--reps", type=int, default=20)
     k = sub.add_parser("counters")
     k.add_argument("--csv", required=True)
     k.add_argument("--key", required=True)
@@ -381,7 +426,7 @@ def main(argv=None):
     e.add_argument("--log", required=True)
     e.add_argument("--out")
     a = ap.parse_args(argv)
-    {"copy": _copy, "gemm": _gemm, "counters": _counters, "stats": _stats, "traffic": _traffic, "mfma": _mfma,
+    {"copy": _copy, "gemm": _gemm, "moe": _moe, "counters": _counters, "stats": _stats, "traffic": _traffic, "mfma": _mfma,
      "valu": _valu, "sweep": _sweep, "spec": _spec}[a.cmd_name](a)
 
 
