@@ -41,6 +41,7 @@ namespace {
 constexpr int KT = 128;                 // weights of a row per k-tile
 constexpr int XT_BYTES = 2 * KT;        // a row's split activations of half a k-tile: 64 hi, 64 lo
 constexpr int KT_BYTES = 2 * XT_BYTES;
+constexpr int WL_ROWS = 74;             // rows of a wavefront in LDS: 64, and those a half's last load has too many
 constexpr int MOE_E_MAX = QMM_MOE_MAX_EXPERTS;
 
 // --------------------------------------------------------------- decoders ----
@@ -49,11 +50,14 @@ constexpr int MOE_E_MAX = QMM_MOE_MAX_EXPERTS;
 // the 8 weights kbase(2 s + kh) + sigma(j), sigma = (0 2 1 3 4 6 5 7): the
 // order in which a dword's bytes unpack pairwise.  The split activations are
 // written in the same order.
-//   LP, TB      a k-tile's main bytes of a row: LP lanes x 16 bytes, row offset TB(kt)
-//   ROW         bytes a row's raw k-tile takes in LDS (a multiple of 16 whose
+//   LP          pieces of 16 bytes that a row's k-tile is loaded in, one lane each:
+//               everything a step needs, headers and scales too: loaded by instructions
+//               of their own these touch every cache line again (gate/up of 8 tokens, 2
+//               of 8 experts 14336 x 4096: Q6_K 260 us against 291, Q8_0 254 / 279,
+//               Q5_K 213 / 240, Q4_K 180 / 186)
+//   TB, at, odd piece j of k-tile kt of a row: byte TB(kt) + at(j), + odd(j) for odd kt
+//   ROW         bytes a row's pieces take in LDS, back to back (a multiple of 16 whose
 //               dwords step through all banks: 16 rows' 16-byte reads never collide)
-//   Extra       the bytes of a row outside the main ones: loaded by the row's two
-//               lanes (kh = 0, 1), stored to LDS behind the main bytes
 //   NW          raw dwords per row and k-tile in registers
 //   STEPS       steps per chain (one scale); step(i): the i-th step to run
 //   NG          groups of raw dwords, group g read from LDS while group g - 1 runs
@@ -108,11 +112,10 @@ template <> struct MDec<QMM_Q4_0> {
     __host__ __device__ static int kbase(int p) { return kbase_nibble(p); }
     __host__ __device__ static float xscale(int p) { return (p >> 1) & 1 ? 0.0625f : 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    static constexpr int LP = 4, ROW = 80;
+    static constexpr int LP = 5, ROW = 80;  // 72 bytes
     __device__ static uint32_t TB(int kt) { return 72u * (uint32_t)kt; }
-    struct Extra { uint32_t v; };  // bytes 64 .. 71
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) { x.v = ld32(rs, row + 64u + 4u * kh, TB(kt)); }
-    __device__ static void store(uint8_t *p, int kh, const Extra &x) { *reinterpret_cast<uint32_t *>(p + 64 + 4 * kh) = x.v; }
+    __device__ static uint32_t at(int j) { return 16u * (uint32_t)j; }
+    __device__ static uint32_t odd(int) { return 0u; }
     __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
         if (g & 1) lds_dwords<2, false>(p + 18 * g + 2 + 8 * kh, &r[3 * g]);
         else lds_dwords<2, true>(p + 18 * g + 2 + 8 * kh, &r[3 * g]);
@@ -134,11 +137,10 @@ template <> struct MDec<QMM_Q4_1> {
     __host__ __device__ static int kbase(int p) { return kbase_nibble(p); }
     __host__ __device__ static float xscale(int p) { return (p >> 1) & 1 ? 0.0625f : 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    static constexpr int LP = 4, ROW = 80;
+    static constexpr int LP = 5, ROW = 80;
     __device__ static uint32_t TB(int kt) { return 80u * (uint32_t)kt; }
-    struct Extra { u32x2_t v; };  // bytes 64 .. 79
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) { x.v = ld64(rs, row + 64u + 8u * kh, TB(kt)); }
-    __device__ static void store(uint8_t *p, int kh, const Extra &x) { *reinterpret_cast<u32x2_t *>(p + 64 + 8 * kh) = x.v; }
+    __device__ static uint32_t at(int j) { return 16u * (uint32_t)j; }
+    __device__ static uint32_t odd(int) { return 0u; }
     __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
         lds_dwords<2, false>(p + 20 * g + 4 + 8 * kh, &r[3 * g]);
         r[3 * g + 2] = at32(p + 20 * g);
@@ -170,11 +172,10 @@ template <> struct MDec<QMM_Q8_0> {
     __host__ __device__ static int kbase(int p) { return 32 * (p >> 2) + 16 * (p & 1) + 8 * ((p >> 1) & 1); }
     __host__ __device__ static float xscale(int) { return 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    static constexpr int LP = 8, ROW = 144;
+    static constexpr int LP = 9, ROW = 144;  // 136 bytes
     __device__ static uint32_t TB(int kt) { return 136u * (uint32_t)kt; }
-    struct Extra { uint32_t v; };  // bytes 128 .. 135
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) { x.v = ld32(rs, row + 128u + 4u * kh, TB(kt)); }
-    __device__ static void store(uint8_t *p, int kh, const Extra &x) { *reinterpret_cast<uint32_t *>(p + 128 + 4 * kh) = x.v; }
+    __device__ static uint32_t at(int j) { return 16u * (uint32_t)j; }
+    __device__ static uint32_t odd(int) { return 0u; }
     __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
         if (g & 1) lds_dwords<4, false>(p + 34 * g + 2 + 16 * kh, &r[5 * g]);
         else lds_dwords<4, true>(p + 34 * g + 2 + 16 * kh, &r[5 * g]);
@@ -217,19 +218,11 @@ struct MDecK {
     __host__ __device__ static int kbase(int p) { return kbase_k(p); }
     __host__ __device__ static float xscale(int) { return 1.0f; }
     __host__ __device__ static constexpr int step(int i) { return i; }
-    // LDS row: the 64 code bytes of the half super-block, qh[32] (Q5_K), the header
-    static constexpr int LP = 4, ROW = QH ? 112 : 80;
-    __device__ static uint32_t TB(int kt) { return (uint32_t)BB * (uint32_t)(kt >> 1) + 16u + 32u * QH + 64u * (kt & 1); }
-    struct Extra { u32x2_t h; u32x4_t q; };
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) {
-        const uint32_t sb = (uint32_t)BB * (uint32_t)(kt >> 1);
-        x.h = ld64(rs, row + 8u * kh, sb);
-        if constexpr (QH) x.q = ld128(rs, row + 16u + 16u * kh, sb);
-    }
-    __device__ static void store(uint8_t *p, int kh, const Extra &x) {
-        *reinterpret_cast<u32x2_t *>(p + ROW - 16 + 8 * kh) = x.h;
-        if constexpr (QH) *reinterpret_cast<u32x4_t *>(p + 64 + 16 * kh) = x.q;
-    }
+    // pieces: the 64 code bytes of the half super-block, qh[32] (Q5_K), the header
+    static constexpr int LP = QH ? 7 : 5, ROW = 16 * LP;
+    __device__ static uint32_t TB(int kt) { return (uint32_t)BB * (uint32_t)(kt >> 1); }
+    __device__ static uint32_t at(int j) { return j < 4 ? 16u + 32u * QH + 16u * (uint32_t)j : j < LP - 1 ? 16u * (uint32_t)(j - 3) : 0u; }
+    __device__ static uint32_t odd(int j) { return j < 4 ? 64u : 0u; }
     __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
         const u32x4_t q = at128(p + 32 * g + 16 * kh);
         r[4 + 4 * g] = q.x; r[5 + 4 * g] = q.y; r[6 + 4 * g] = q.z; r[7 + 4 * g] = q.w;
@@ -290,28 +283,19 @@ template <> struct MDec<QMM_Q6_K> {
     __host__ __device__ static constexpr int step(int i) { return 2 * (i & 3) + (i >> 2); }
     __host__ __device__ static int kbase(int p) { return 16 * step(p >> 1) + 8 * (p & 1); }
     __host__ __device__ static float xscale(int) { return 1.0f; }
-    // LDS row: ql[64] of the half, qh[32], the 8 sub-scales, d
-    static constexpr int LP = 4, ROW = 112;
-    __device__ static uint32_t TB(int kt) { return 210u * (uint32_t)(kt >> 1) + 64u * (kt & 1); }
-    struct Extra { u32x4_t q; uint32_t sc, d; };
-    __device__ static void load(Rsrc rs, uint32_t row, int kt, int kh, Extra &x) {
-        const uint32_t sb = 210u * (uint32_t)(kt >> 1), h = kt & 1;
-        x.q = ld128(rs, row + 128u + 16u * kh, sb + 32u * h);
-        x.sc = ld32(rs, row + 192u + 4u * kh, sb + 8u * h);
-        x.d = ld16(rs, row + 208u, sb);
-    }
-    __device__ static void store(uint8_t *p, int kh, const Extra &x) {
-        *reinterpret_cast<u32x4_t *>(p + 64 + 16 * kh) = x.q;
-        *reinterpret_cast<uint32_t *>(p + 96 + 4 * kh) = x.sc;
-        *reinterpret_cast<uint32_t *>(p + 104 + 4 * kh) = x.d;  // both lanes: a branch here costs registers
-    }
+    // pieces: ql[64] of the half, qh[32], its 8 sub-scales (and 8 bytes more), the
+    // super-block's last 16 bytes, which d ends
+    static constexpr int LP = 8, ROW = 144;
+    __device__ static uint32_t TB(int kt) { return 210u * (uint32_t)(kt >> 1); }
+    __device__ static uint32_t at(int j) { return j < 4 ? 16u * (uint32_t)j : j < 6 ? 64u + 16u * (uint32_t)j : j == 6 ? 192u : 194u; }
+    __device__ static uint32_t odd(int j) { return j < 4 ? 64u : j < 6 ? 32u : j == 6 ? 8u : 0u; }
     __device__ static void read(const uint8_t *p, int kh, int g, uint32_t (&r)[NW]) {
         const u32x2_t a = at64(p + 16 * g + 8 * kh), b = at64(p + 32 + 16 * g + 8 * kh), c = at64(p + 64 + 16 * g + 8 * kh);
         r[6 * g] = a.x; r[6 * g + 1] = a.y; r[6 * g + 2] = b.x; r[6 * g + 3] = b.y; r[6 * g + 4] = c.x; r[6 * g + 5] = c.y;
         if (g == 0) {
             const u32x2_t sc = at64(p + 96);
             r[12] = sc.x; r[13] = sc.y;
-            r[14] = at32(p + 104);
+            r[14] = at16(p + 126);
         }
     }
     __device__ static void prep(const uint32_t (&r)[NW], int, int, Pre &p) {
@@ -539,20 +523,25 @@ struct MoeGemmArgs {
 
 // k-tiles [k0, k1) of one job: W wavefronts, each 2 x 32 rows of the matrix
 // (swiglu: 32 gate rows and the same 32 up rows) against the n_rows <= 32 FN
-// slots of a tile.  Weights: a wavefront loads its own rows' bytes of a k-tile in
-// runs of 64 or 128 bytes (lanes reading a row each would touch 32 cache lines
-// per instruction), parks them in its part of LDS one k-tile ahead and reads each
+// slots of a tile.  Weights: a wavefront loads its own rows' bytes of a k-tile, 5
+// to 9 lanes next to each other on a row (lanes reading a row each would touch
+// 32 cache lines per instruction), parks them in its part of LDS one k-tile ahead and reads each
 // lane's bytes from there.  Activations: all wavefronts share the tile's rows,
 // double-buffered.
 template <int DT, int FN, int BN, int W, bool SWI>
 __device__ __forceinline__ void moe_tile(const MoeGemmArgs &a, const int4 tile, int e, int n_rows, int mt, int split, int k0, int k1,
-                                         uint8_t (*xl)[BN * XT_BYTES], uint8_t (*wl)[64 * MDec<DT>::ROW], int32_t *slot_of,
+                                         uint8_t (*xl)[BN * XT_BYTES], uint8_t (*wl)[WL_ROWS * MDec<DT>::ROW], int32_t *slot_of,
                                          float *rsc) {
     using D = MDec<DT>;
     constexpr int FR = 32 * FN, RW = SWI ? 32 : 64, BM = RW * W;
     constexpr int NP = FR * 16 / (64 * W);  // 16-byte pieces of half a k-tile per thread
     static_assert(NP >= 1, "tile too small for the workgroup");
-    constexpr int RI = 64 / D::LP, MI = 64 / RI;  // rows per main load instruction, instructions per k-tile
+    // rows per load instruction (lanes past them start the next row), instructions
+    // per half (gate and up rows come from two blobs) and k-tile
+    constexpr int RI = 64 / D::LP, HALVES = SWI ? 2 : 1, MH = (64 / HALVES + RI - 1) / RI, MI = HALVES * MH;
+    constexpr int HROWS = (MH - 1) * RI + 63 / D::LP + 1;  // rows that a half's loads bring
+    constexpr int HALF2 = SWI ? HROWS : 32;                // the second 32 rows' first in LDS
+    static_assert(HALVES * HROWS <= WL_ROWS, "rows behind the last overrun the wavefront's LDS");
     const int t = (int)threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l32 = lane & 31, kh = lane >> 5;
     for (int i = t; i < FR; i += 64 * W) {
@@ -587,10 +576,10 @@ __device__ __forceinline__ void moe_tile(const MoeGemmArgs &a, const int4 tile, 
     const Rsrc wr1 = SWI ? make_rsrc_uniform(a.w1 + (base - mis), nb0) : wr0;
     const uint32_t rb = (uint32_t)a.row_bytes;
     const uint32_t so1 = SWI ? 0u : 32u * rb;   // the second 32 rows: of the up matrix, or further down
-    const uint32_t moff = mis + (uint32_t)(lane / D::LP) * rb + 16u * (uint32_t)(lane % D::LP);
-    const uint32_t eoff = mis + (uint32_t)l32 * rb;
+    const uint32_t moff = mis + (uint32_t)(lane / D::LP) * rb + D::at(lane % D::LP);
+    const uint32_t modd = D::odd(lane % D::LP);
     uint8_t *const wmain = &wl[wave][(lane / D::LP) * D::ROW + 16 * (lane % D::LP)];
-    uint8_t *const wrow[2] = {&wl[wave][l32 * D::ROW], &wl[wave][(32 + l32) * D::ROW]};
+    uint8_t *const wrow[2] = {&wl[wave][l32 * D::ROW], &wl[wave][(HALF2 + l32) * D::ROW]};
 
     // block sums of the lane's slots (formats with minima): lane half 0 alone
     uint32_t sumoff[FN];
@@ -611,17 +600,14 @@ __device__ __forceinline__ void moe_tile(const MoeGemmArgs &a, const int4 tile, 
 #pragma unroll
             for (int j = 0; j < 16; j++) acc[i][f][j] = 0.f;
 
+    // Rows past a half's last are behind the resource's end (zeros) and have
+    // their own place in LDS.
     u32x4_t wm[MI];
-    typename D::Extra wx[2];
     auto fetch_w = [&](int kt) {
-        const uint32_t tb = D::TB(kt);
+        const uint32_t tb = D::TB(kt), off = moff + (kt & 1 ? modd : 0u);
 #pragma unroll
-        for (int i = 0; i < MI; i++) {
-            const int h = i / (MI / 2), r = (i % (MI / 2)) * RI;
-            wm[i] = ld128(h ? wr1 : wr0, moff, tb + (h ? so1 : 0u) + (uint32_t)r * rb);
-        }
-        D::load(wr0, eoff, kt, kh, wx[0]);
-        D::load(wr1, eoff + so1, kt, kh, wx[1]);
+        for (int i = 0; i < MI; i++)
+            wm[i] = ld128(i >= MH ? wr1 : wr0, off, tb + (uint32_t)(i % MH * RI) * rb);
     };
     // A row of 18- or 34-byte blocks may end inside a dword, which reads as 0
     // where it reaches past the matrix: its last two bytes are loaded by
@@ -630,14 +616,13 @@ __device__ __forceinline__ void moe_tile(const MoeGemmArgs &a, const int4 tile, 
     constexpr bool TAIL = DT == QMM_Q4_0 || DT == QMM_Q8_0;
     uint32_t tail[2] = {0u, 0u};
     if constexpr (TAIL) {
-        tail[0] = ld16(wr0, eoff + rb - 2u, 0u);
-        tail[1] = ld16(wr1, eoff + so1 + rb - 2u, 0u);
+        const uint32_t end = mis + (uint32_t)l32 * rb + rb - 2u;
+        tail[0] = ld16(wr0, end, 0u);
+        tail[1] = ld16(wr1, end + so1, 0u);
     }
     auto store_w = [&](int kt) {
 #pragma unroll
-        for (int i = 0; i < MI; i++) *reinterpret_cast<u32x4_t *>(wmain + i * RI * D::ROW) = wm[i];
-        D::store(wrow[0], kh, wx[0]);
-        D::store(wrow[1], kh, wx[1]);
+        for (int i = 0; i < MI; i++) *reinterpret_cast<u32x4_t *>(wmain + (i / MH * HALF2 + i % MH * RI) * D::ROW) = wm[i];
         if constexpr (TAIL) {
             const int at = kt == a.nkt - 1 ? (int)rb - (int)D::TB(kt) - 2 : D::ROW - 4;
             *reinterpret_cast<uint16_t *>(wrow[0] + at) = (uint16_t)tail[0];
@@ -814,7 +799,7 @@ template <int DT, int FN, int W, bool SWI>
 __global__ void __launch_bounds__(64 * W, 2) moe_gemm_kernel(const MoeGemmArgs a) {
     constexpr int BN = 32 * FN;
     __shared__ __attribute__((aligned(16))) uint8_t xl[2][BN * XT_BYTES];           // two half k-tiles of activations
-    __shared__ __attribute__((aligned(16))) uint8_t wl[W][64 * MDec<DT>::ROW];      // each wavefront's rows
+    __shared__ __attribute__((aligned(16))) uint8_t wl[W][WL_ROWS * MDec<DT>::ROW];  // each wavefront's rows
     __shared__ int32_t slot_of[BN];
     __shared__ float rsc[BN];
     // An XCD (workgroup id mod 8) takes a run of jobs, ordered by expert, then
