@@ -19,6 +19,7 @@
 // a row meet in LDS and are added in item order, so the down projection's sum
 // over a token's experts needs no second pass and no atomics.
 #include <algorithm>
+#include <cmath>
 
 #include "qmm_device.hpp"
 #include "qmm_internal.hpp"
@@ -267,25 +268,37 @@ hipError_t run_gemv(const void *w0, const void *w1, int64_t E, int64_t M, int64_
     return hipGetLastError();
 }
 
-// Which form: the few-token kernel reads an expert's bytes for every slot (4 to 5
-// TB/s), the matrix cores once per touched expert (2 to 2.5 TB/s while memory
-// bounds them) after two more launches (about 20 us).  With S slots over E
-// experts the two meet at S = 2 E, where an expert that is touched has 2.3
-// slots: 64 experts, 8 of them each, gate/up 1024 x 2048 Q4_K, 16 tokens: 57
-// against 60 us (8: 33 against 54, 24: 88 against 61); 8 experts, 2 each, 14336 x
-// 4096: 8 tokens 198 against 190 us (4: 108 against 138, 16: 365 against 205).
-// Below 80 MB of reads in all the few-token kernel is done before the other
-// form's launches are.  A measurement build takes QMM_MOE_GEMM_FROM_N = n to
-// decide by the tokens alone.
+// Which form, by what the two take.  The few-token kernel spends every slot's
+// expert again: its bytes at r1, rows counted as the lanes they occupy (a row of 4
+// units takes 16 lanes), and 5 ns for its workgroups.  The matrix cores take 20 us
+// for their launches and every touched expert's bytes once, at r2; of E experts S
+// slots touch about E (1 - e^(-S/E)).  The rates are those measured while either
+// form is slower than its launches (TB/s; caches serve an expert's second slot, so
+// r1 can pass the memory's rate).  Few tokens against matrix cores, measured:
+//   64 experts, 8 each, gate/up 1024 x 2048, 16 and 24 tokens: Q4_0 51 / 60 us and
+//   71 / 62, Q4_K 60 / 53 and 85 / 54, Q8_0 72 / 74 and 102 / 75; down 2048 x 1024:
+//   Q8_0 35 / 48 and 52 / 50, Q6_K 36 / 50 and 55 / 51
+//   8 experts, 2 each, gate/up 14336 x 4096, 4, 8 and 12 tokens: Q4_0 92 / 142, 169 /
+//   185, 243 / 198; Q4_K 109 / 128, 204 / 174, 296 / 187; Q6_K 130 / 198, 253 / 257,
+//   376 / 273
+//   16 experts, 4 each, gate/up 256 x 256 Q4_K, 1024 tokens: 181 / 22
+// A measurement build takes QMM_MOE_GEMM_FROM_N = n to decide by the tokens alone.
 bool use_gemm(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, bool down) {
     static const int lever = tuning_lever("QMM_MOE_GEMM_FROM_N", 0);
     if (lever) return N >= lever;
-    const int64_t S = N * T;
-    if (S > (int64_t(1) << 30) / M) return true;  // the few-token grid's limit
-    const int bs = dtype == QMM_Q4_K || dtype == QMM_Q5_K || dtype == QMM_Q6_K ? 256 : 32;
-    const int bb = dtype == QMM_Q4_0 ? 18 : dtype == QMM_Q4_1 ? 20 : dtype == QMM_Q8_0 ? 34 : dtype == QMM_Q4_K ? 144 : dtype == QMM_Q5_K ? 176 : 210;
-    const int64_t row = K / bs * bb, expert = (down ? 1 : 2) * M * row;
-    return S >= 2 * E && expert >= (int64_t(80) << 20) / S;
+    if (N * T > (int64_t(1) << 30) / M) return true;  // the few-token kernel's grid
+    struct Rate { int bs, bb; double r1, r2; };
+    const Rate f = dtype == QMM_Q4_0   ? Rate{32, 18, 6.0, 2.8}
+                   : dtype == QMM_Q4_1 ? Rate{32, 20, 6.0, 3.0}
+                   : dtype == QMM_Q8_0 ? Rate{32, 34, 7.5, 3.8}
+                   : dtype == QMM_Q4_K ? Rate{256, 144, 5.0, 3.5}
+                   : dtype == QMM_Q5_K ? Rate{256, 176, 5.0, 3.4}
+                                       : Rate{256, 210, 6.0, 3.0};
+    const int64_t U = (K + 63) / 64, lanes = U <= 16 ? 16 : U <= 32 ? 32 : (U + 63) / 64 * 64;
+    const double S = (double)(N * T), rows = (down ? 1.0 : 2.0) * (double)M, per = (double)f.bb / f.bs * 1e-6;  // MB a weight
+    const double few = S * (rows * 64.0 * (double)lanes * per / f.r1 + 0.005);
+    const double many = 20.0 + (double)E * (1.0 - std::exp(-S / (double)E)) * rows * (double)K * per / f.r2;
+    return few > many;
 }
 
 }  // namespace
