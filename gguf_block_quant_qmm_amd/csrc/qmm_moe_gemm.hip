@@ -20,12 +20,12 @@
 // projection, the weighted sum over a token's slots in slot order (for gate/up
 // with a shared K, silu(gate) * up of the summed shares).
 //
-// Measured, 512 tokens: gate/up of 2 of 8 experts 14336 x 4096 Q4_K 605-630 us,
-// 390 TFLOP/s of the formula's operations, 780 of the matrix cores' (a large f16
-// product reaches 1130-1280 here); 530 where every tile is full.  Down of 8 of 64
-// experts 4096 x 1024 Q8_0 176-187 us, 33 tokens gate/up of 4 of 60 experts 1408 x
-// 2048 Q6_K 91 us.  Taken out one at a time, the Q4_K case (640 us then) loses 113
-// us with the weights' loads and stores, 75 with the activations', 47 with the
+// Measured, 512 tokens: gate/up of 2 of 8 experts 14336 x 4096 Q4_K 580-600 us,
+// 410 TFLOP/s of the formula's operations, 820 of the matrix cores' (a large f16
+// product reaches 1130-1280 here).  Down of 8 of 64
+// experts 4096 x 1024 Q8_0 176-181 us, 33 tokens gate/up of 4 of 60 experts 1408 x
+// 2048 Q6_K 84 us.  Taken out one at a time, the Q4_K case lost, at 640 us, 113 us
+// with the weights' loads and stores, 75 with the activations', 47 with the
 // barriers, 47 with the minima, 13 with the decoding; the matrix steps and the
 // barriers alone take 412.
 #include <algorithm>
