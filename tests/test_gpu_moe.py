@@ -194,6 +194,19 @@ def test_shared_k_on_matrix_cores(dt):
         check_down(dt, 2, M, K, N, 2)
 
 
+@pytest.mark.parametrize("E", [65, 200, 1024])
+@pytest.mark.parametrize("dt", [q.QMM_Q4_0, q.QMM_Q4_K], ids=lambda d: NAMES[d])
+def test_many_experts(dt, E):
+    """More experts than a wavefront has lanes, in both forms; the last expert has slots."""
+    M, K, T = 40, 256, 8
+    for need, check in ((q.moe_swiglu_work_bytes, check_swiglu), (q.moe_down_work_bytes, check_down)):
+        for N in (1, 3, tokens_on_matrix_cores(need, dt, E, M, K, T)):
+            g = np.random.default_rng([E, N])
+            ids = g.integers(0, E, (N, T), dtype=np.int32)
+            ids[0, 0], ids[-1, -1] = E - 1, -1
+            check(dt, E, M, K, N, T, ids=ids)
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 8, 9, 31, 32])
 def test_slots_per_token(T):
     for N in (1, 2, 40):
