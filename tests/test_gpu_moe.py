@@ -417,3 +417,28 @@ def test_long_inputs_run_in_passes():
         want = (w[..., None] * y).sum(1)
         tol = (w.abs()[..., None] * TAU * S).sum(1) + (T + 1) * 2.0 ** -24 * (w[..., None] * y).abs().sum(1)
         assert torch.all((Y[lo:hi].double() - want).abs() <= tol)
+
+
+def test_long_gate_up_inputs_run_in_passes():
+    """The same for gate/up, whose passes write their slots' rows at once."""
+    dt, E, M, K, T = q.QMM_Q8_0, 2, 3, 32, 2
+    N = (1 << 21) + 5
+    work = work_of(q.moe_swiglu_work_bytes(dt, E, M, K, N, T))
+    assert work is not None and work.numel() < 2 * q.moe_swiglu_work_bytes(dt, E, M, K, 1 << 21, T)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.randint(-1, E, (N, T), device="cuda", dtype=torch.int32, generator=g)
+    X = torch.randn(N, K, device="cuda", generator=g)
+    blobs = [experts(dt, E, M, K, s) for s in (0, 1)]
+    out = torch.full((N * T + 1, M), 7.0, device="cuda")
+    q.qmm_moe_swiglu(dev(blobs[0]), dev(blobs[1]), dt, E, M, K, N, T, ids, X, out[:N * T], work=work)
+    torch.cuda.synchronize()
+    assert torch.all(out[N * T] == 7.0)
+    W = [torch.from_numpy(oracle.dequant(dt, b, E * M, K)).cuda().view(E, M, K) for b in blobs]
+    for lo, hi in ((0, 500), ((1 << 21) - 300, N)):
+        i, x = ids[lo:hi], X[lo:hi, None, None].double()
+        live = (i >= 0)[..., None, None]
+        (gv, Sg), (uv, Su) = (((w * x).sum(3), (w * x).abs().sum(3)) for w in (torch.where(live, w[i.clamp(min=0).long()], 0.0) for w in W))
+        want = gv * torch.sigmoid(gv) * uv
+        tol = TAU * (1.1 * Sg * (uv.abs() + TAU * Su) + (gv * torch.sigmoid(gv)).abs() * Su) + 4 * 2.0 ** -24 * want.abs()
+        got = out[lo * T:hi * T].view(hi - lo, T, M).double()
+        assert torch.all((got - want).abs() <= tol)
