@@ -423,7 +423,8 @@ int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, 
  * A non-finite activation makes that token's outputs non-finite (a matrix-core
  * step also multiplies it by zero codes: NaN where the sum would be infinite)
  * and no other token's.  Every slot's result is the same whatever other slots
- * the call holds, as long as the form is the same.  1 <= E <= QMM_MOE_MAX_EXPERTS,
+ * the call holds, as long as dtype, E, M, K, N and T are the same (they choose the
+ * form and how K is shared out).  1 <= E <= QMM_MOE_MAX_EXPERTS,
  * 1 <= T <= QMM_MOE_MAX_TOPK, N * T <= 2^31 - 1, M <= QMM_MOE_MAX_ROWS, K any
  * multiple of the block size up to QMM_MOE_MAX_K. */
 int64_t qmm_moe_swiglu_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T);
