@@ -420,6 +420,9 @@ int qmm_moe_route(const float *logits, const float *bias, int64_t N, int64_t E, 
  *                 Q5_K counted apart from the codes); the activations are split in
  *                 two f16 parts under a power of two per row, so only a row whose
  *                 values span more than 2^20 notices the second term.
+ * Either adds 2^-125 sum_k |w| + K 2^-149, what products below f32's normal
+ * range lose: nothing to see while |x| >= 2^-100, all of the value near f32's
+ * smallest.
  * A non-finite activation makes that token's outputs non-finite (a matrix-core
  * step also multiplies it by zero codes: NaN where the sum would be infinite)
  * and no other token's.  Every slot's result is the same whatever other slots
