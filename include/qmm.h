@@ -356,8 +356,8 @@ int qmm_gemm_repacked_kernel(int dtype, int64_t M, int64_t K, int64_t N);
  *   H            device f32 [N][K] or NULL
  *   scales, quants  device f32 [N][K/32] and int8 [N][K] as qmm_quantize_q8_0
  *                writes them, or both NULL; need K a multiple of 32
- * With neither H nor quants only residual_out is written.  block, w_post and
- * gate without a block are ignored.  Apart from residual_out == residual the
+ * With neither H nor quants only residual_out is written.  w_post and gate
+ * without a block are ignored.  Apart from residual_out == residual the
  * outputs overlap nothing.  1 <= N <= 2^31 - 1, 1 <= K <= 2^28; every pointer
  * 16-B aligned. */
 int qmm_block_norm(const float *block, const float *w_post, const float *gate, int64_t gate_stride, double scale,
@@ -374,7 +374,9 @@ int qmm_block_norm(const float *block, const float *w_post, const float *gate, i
  *   if the sum is 0), times scale; rounded to f32 once.
  * A logit of -inf or NaN masks its expert: score 0, and behind every expert
  * with a larger c.  A row of nothing but those has scores 0.  A logit of +inf
- * counts as the largest finite f32.  A NaN in c counts as -inf.
+ * counts as the largest finite f32.  A NaN in c counts as -inf, and so does a
+ * group's score that is one: +inf and -inf in a group's two largest c (biases of
+ * both kinds) put it behind every group with a larger score.
  *   logits   device f32 [N][E], 4-B aligned
  *   bias     device f32 [E] (a balance bias: it moves the choice, not the
  *            weights), 4-B aligned, or NULL
