@@ -33,6 +33,11 @@ Subcommands (run from the repository root):
            and qmm_moe_down (K x M) with the residual; random blobs of one
            dtype, enough copies of the three expert tensors to fill 1 GiB.
 
+  case     --name swiglu_prefill --reps R
+           Runs one listed case of perf/operators.py R times through the
+           library, over inputs of as many seeds as fill 1 GiB (at most 16:
+           the small cases' inputs stay in the caches).
+
   counters --csv <counter_collection.csv> --key REGEX --title T --cmd C
            Markdown table of every counter in a --pmc run, the mean per
            dispatch (summed over the device) of the dispatches whose kernel
@@ -135,6 +140,24 @@ def _moe(args):
         q.qmm_moe_down(down, dt, E, K, M, N, T, ids, wt, act, y, residual=y, work=work)
     torch.cuda.synchronize()
     print(f"sparse block {args.dtype} E={E} {M}x{K} N={N} T={T} x {args.reps} (work {nb} bytes, {len(sets)} copies)", flush=True)
+
+
+def _case(args):
+    import torch
+
+    from perf import operators
+    cases = {c["name"]: c for c in operators.listed()}
+    if args.name not in cases:
+        raise SystemExit(f"no case {args.name!r}; listed are {', '.join(cases)}")
+    operators.own = True
+    states, held = [], 0
+    while held < 1 << 30 and len(states) < 16:
+        states.append(operators.prepare(cases[args.name], len(states)))
+        held += sum(v.nbytes for v in states[-1].values() if isinstance(v, torch.Tensor))
+    for r in range(args.reps):
+        operators.run(states[r % len(states)])
+    torch.cuda.synchronize()
+    print(f"case {args.name} x {args.reps} ({len(states)} inputs, {held >> 20} MiB)", flush=True)
 
 
 def _counters(args):
@@ -401,6 +424,9 @@ def main(argv=None):
     o.add_argument("--N", type=int, default=512)
     o.add_argument("--T", type=int, default=2)
     o.add_argument("--reps", type=int, default=20)
+    n = sub.add_parser("case")
+    n.add_argument("--name", required=True)
+    n.add_argument("--reps", type=int, default=20)
     k = sub.add_parser("counters")
     k.add_argument("--csv", required=True)
     k.add_argument("--key", required=True)
@@ -426,7 +452,7 @@ def main(argv=None):
     e.add_argument("--log", required=True)
     e.add_argument("--out")
     a = ap.parse_args(argv)
-    {"copy": _copy, "gemm": _gemm, "moe": _moe, "counters": _counters, "stats": _stats, "traffic": _traffic, "mfma": _mfma,
+    {"copy": _copy, "gemm": _gemm, "moe": _moe, "case": _case, "counters": _counters, "stats": _stats, "traffic": _traffic, "mfma": _mfma,
      "valu": _valu, "sweep": _sweep, "spec": _spec}[a.cmd_name](a)
 
 
