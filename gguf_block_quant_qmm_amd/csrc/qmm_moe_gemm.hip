@@ -3,8 +3,11 @@
 //
 // Exact codes, split activations.  An f32 activation row is scaled by a power
 // of two so that its largest value lies in [2^9, 2^10) and split into two
-// f16 numbers, x = hi + lo with |x - hi - lo| <= 2^-24 |x| (2^-25 absolute
-// where lo is subnormal).  The weights enter as the integers they are made of,
+// f16 numbers, x = hi + lo with |x - hi - lo| <= 2^-23 |x| (what an 11-bit hi
+// leaves of 24 bits takes up to 12, lo holds 11), or 2^-25 absolute where lo is
+// subnormal; high nibbles of Q4_0 and Q4_1 enter as 16 times their code against
+// x / 16, where that is 2^-21, at most 2^-30 of the row's largest value.  The
+// weights enter as the integers they are made of,
 // exact in f16: q - 8 (Q4_0), q (Q8_0, Q4_1), sc * q (Q4_K, Q5_K: at most
 // 63 * 31 < 2^11), q - 32 (Q6_K).  v_mfma_f32_32x32x16_f16 multiplies codes by
 // hi and by lo into one f32 sum per block (a chain of steps that share one
