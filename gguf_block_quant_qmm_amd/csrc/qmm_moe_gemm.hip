@@ -87,7 +87,6 @@ __device__ __forceinline__ half2v byte13_code(uint32_t w, float bias) { return b
 
 __device__ __forceinline__ uint32_t ld16(Rsrc rs, uint32_t off, uint32_t so) { return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, off, so, 0); }
 __device__ __forceinline__ uint32_t ld32(Rsrc rs, uint32_t off, uint32_t so) { return __builtin_amdgcn_raw_buffer_load_b32(rs, off, so, 0); }
-__device__ __forceinline__ u32x2_t ld64(Rsrc rs, uint32_t off, uint32_t so) { return __builtin_amdgcn_raw_buffer_load_b64(rs, off, so, 0); }
 __device__ __forceinline__ u32x4_t ld128(Rsrc rs, uint32_t off, uint32_t so) { return __builtin_amdgcn_raw_buffer_load_b128(rs, off, so, 0); }
 __device__ __forceinline__ uint32_t at32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 __device__ __forceinline__ uint32_t at16(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
