@@ -4,10 +4,14 @@
 //
 // Few tokens: the GEMV's f32 arithmetic (qmm_units.hpp), memory-bound on the
 // chosen experts' bytes.  Many tokens: the matrix cores (qmm_moe_gemm.hip).
-// Measured, gate/up of 1 token, 2 of 8 experts 14336 x 4096: Q4_0 25 us (5.2 TB/s),
-// Q8_0 48 us (5.2), Q6_K 41 us (4.7); down of 2 of 8 experts 4096 x 14336 Q6_K
-// 22 us (4.3).  The K-quants' decoding costs more than the reads wait: down of 7
-// tokens, 8 of 64 experts 4096 x 1024 Q5_K, 38 us (4.2 TB/s), 28 of them VALU issue.
+// Measured, us and fetched TB/s of a launch (profiler's medians, the experts'
+// tensors rotating through 1 GiB), 1 token, 2 of 8 experts, gate/up 14336 x 4096 and
+// down 4096 x 14336: Q4_0 28.4 (4.7) and 17.3 (3.9), Q4_1 31.8 (4.6) and 20.2 (3.7),
+// Q4_K 31.7 (4.2) and 20.6 (3.3), Q5_K 37.3 (4.3) and 25.0 (3.3), Q8_0 44.6 (5.6) and
+// 27.7 (4.5), Q6_K 35.2 (5.5) and 22.7 (4.3).  The K-quants' decoding costs more than
+// the reads wait: down of 7 tokens, 8 of 64 experts 4096 x 1024 Q5_K, 40-43 us
+// (3.1-3.3 TB/s), 30 of them VALU issue; on inputs that the caches hold, 35.  Times of
+// two variants beside each other below are from a captured graph over four inputs.
 //
 // The few-token kernel cuts a row into units of 64 weights, one per lane, as
 // the GEMV does, but an expert's rows are often short (K of a few hundred
@@ -275,13 +279,18 @@ hipError_t run_gemv(const void *w0, const void *w1, int64_t E, int64_t M, int64_
 // slots touch about E (1 - e^(-S/E)).  The rates are those measured while either
 // form is slower than its launches (TB/s; caches serve an expert's second slot, so
 // r1 can pass the memory's rate).  Few tokens against matrix cores, measured:
-//   64 experts, 8 each, gate/up 1024 x 2048, 16 and 24 tokens: Q4_0 51 / 60 us and
-//   71 / 62, Q4_K 60 / 53 and 85 / 54, Q8_0 72 / 74 and 102 / 75; down 2048 x 1024:
-//   Q8_0 35 / 48 and 52 / 50, Q6_K 36 / 50 and 55 / 51
-//   8 experts, 2 each, gate/up 14336 x 4096, 4, 8 and 12 tokens: Q4_0 92 / 142, 169 /
-//   185, 243 / 198; Q4_K 109 / 128, 204 / 174, 296 / 187; Q6_K 130 / 198, 253 / 257,
-//   376 / 273
-//   16 experts, 4 each, gate/up 256 x 256 Q4_K, 1024 tokens: 181 / 22
+//   64 experts, 8 each, gate/up 1024 x 2048, 16 and 24 tokens: Q4_0 48 / 60 us and
+//   72 / 62, Q4_1 55 / 61 and 76 / 62, Q4_K 61 / 53 and 89 / 55, Q5_K 74 / 64 and 106 /
+//   66, Q8_0 71 / 76 and 102 / 78, Q6_K 68 / 80 and 102 / 81; down 2048 x 1024: Q4_0
+//   28 / 38 and 40 / 39, Q4_1 28 / 37 and 43 / 39, Q4_K 31 / 34 and 47 / 34, Q5_K 40 /
+//   42 and 61 / 43, Q8_0 35 / 48 and 51 / 49, Q6_K 36 / 49 and 55 / 51
+//   8 experts, 2 each, gate/up 14336 x 4096, 4, 8 and 12 tokens: Q4_0 95 / 142, 173 /
+//   185, 240 / 198; Q4_1 104 / 143, 201 / 187, 289 / 197; Q4_K 110 / 127, 208 / 175,
+//   299 / 188; Q5_K 138 / 156, 263 / 213, 386 / 229; Q8_0 136 / 192, 275 / 247, 415 /
+//   263; Q6_K 133 / 198, 262 / 260 (253 / 257 another time), 381 / 272
+//   16 experts, 4 each, gate/up 256 x 256 Q4_K, 1024 tokens: 177 / 21
+// The rule takes the faster one at all of these points but one (down of 24 tokens in
+// Q4_1, 43 against 39).  It counts every slot as live and knows nothing of shared K.
 // A measurement build takes QMM_MOE_GEMM_FROM_N = n to decide by the tokens alone.
 bool use_gemm(int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, bool down) {
     static const int lever = tuning_lever("QMM_MOE_GEMM_FROM_N", 0);

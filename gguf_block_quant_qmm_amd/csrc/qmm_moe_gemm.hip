@@ -23,14 +23,21 @@
 // projection, the weighted sum over a token's slots in slot order (for gate/up
 // with a shared K, silu(gate) * up of the summed shares).
 //
-// Measured, 512 tokens: gate/up of 2 of 8 experts 14336 x 4096 Q4_K 580-600 us,
-// 410 TFLOP/s of the formula's operations, 820 of the matrix cores' (a large f16
-// product reaches 1130-1280 here).  Down of 8 of 64
-// experts 4096 x 1024 Q8_0 176-181 us, 33 tokens gate/up of 4 of 60 experts 1408 x
-// 2048 Q6_K 84 us.  Taken out one at a time, the Q4_K case lost, at 640 us, 113 us
-// with the weights' loads and stores, 75 with the activations', 47 with the
-// barriers, 47 with the minima, 13 with the decoding; the matrix steps and the
-// barriers alone take 412.
+// Measured (profiler's medians of launch (2), the experts' tensors rotating through
+// 1 GiB), 512 tokens, gate/up of 2 of 8 experts 14336 x 4096: Q4_K 593-626 us (the
+// clock drops for the first dozens of launches), 384-405 TFLOP/s of the formula's
+// operations, twice that of the matrix cores' (a large f16 product reaches 1130-1280
+// here); Q4_0 619, Q4_1 652, Q5_K 661, Q8_0 734, Q6_K 846.  512 tokens, 8 of 64
+// experts, Q8_0: gate/up 1024 x 4096 301-339 us, down 4096 x 1024 144-163.  37
+// tokens, gate/up of 4 of 60 experts 1408 x 2048 Q6_K, 83.  It is a sum, not an
+// overlap: the Q4_K case keeps the matrix cores busy for 235 us and issues VALU
+// instructions for 183, along two barriers per k-tile.  Taken out one at a time, it
+// lost, at 640 us, 113 us with the weights' loads and stores, 75 with the
+// activations', 47 with the barriers, 47 with the minima, 13 with the decoding; the
+// matrix steps and the barriers alone take 412.  Launch (1) takes 6 us there, and 80
+// for 4096 tokens of 8 slots, where one workgroup's plan outlasts the row split.
+// Times of two variants beside each other below are from a captured graph over four
+// inputs.
 #include <algorithm>
 
 #include "qmm_device.hpp"
@@ -809,6 +816,11 @@ __device__ __forceinline__ void moe_tile(const MoeGemmArgs &a, const int4 tile, 
         }
 }
 
+// Registers: with two wavefronts per SIMD a lane has 256.  Tiles of 32 slots take
+// 153-194, tiles of 64 239-255, but for Q4_1 and Q6_K, which need 5 to 9 more and keep
+// those in scratch memory (24-40 bytes a lane): 512 tokens of 14336 x 4096 write 68
+// and 121 MB where the outputs are 59.
+//
 // One workgroup per job.  A tile of 64 that holds up to 32 slots, often an
 // expert's last one, runs half of the matrix steps (down of 2 of 8 experts 4096 x
 // 14336 Q6_K, 512 tokens: 685 us against 728 with every tile run in full; of 8 of

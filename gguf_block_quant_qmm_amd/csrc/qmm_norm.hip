@@ -12,13 +12,17 @@
 // vanish in f64.  h is computed from the rounded r, the value that
 // residual_out holds and the next block adds to.
 //
-// Memory-bound: 4096 rows of 4096 (block, residual in; r, h out) take 50 us, 5.3
+// Memory-bound: 4096 rows of 4096 (block, residual in; r, h out) take 51 us, 5.3
 // TB/s, the rate of a large copy on this card (5.1).  One read of the inputs and
 // one write of the outputs: a row of up to 16384 values lives in registers (a
 // wavefront per row up to 1024 values, else a workgroup), the two sums of squares
 // are wavefront reductions with DPP moves joined over the workgroup through LDS in
-// wavefront order.  Longer rows are read again for each pass.  One row of 4096 is
-// bound by latency: load, two sums, store, 3.1 us.
+// wavefront order.  Longer rows are read again for each pass, mostly from the
+// caches (512 rows of 20480: 38 us, 169 MB fetched for 84 MB of inputs).  One row of
+// 4096 is bound by latency: load, two sums, store, 3.1 us (4 to 5 us with a norm
+// after the block, between other launches).  These are the profiler's medians over
+// inputs that rotate through up to 1 GiB; times of two variants beside each other
+// below are from a captured graph over four inputs.
 #include "qmm_device.hpp"
 #include "qmm_internal.hpp"
 #include "qmm_units.hpp"
