@@ -40,6 +40,18 @@ there is no CPU fallback.
                                                      out[n][t] = silu(G_e x_n) * (U_e x_n)
     qmm_moe_down(w, dtype, E, M, K, N, T, ids, weights, H, Y, residual=None, work=None,
                  stream=None)                        Y[n] = residual[n] + sum_t w_nt W_e h_nt
+    qmm_rope_freqs(rot, base, freqs, factor=1.0, context=0.0, beta_fast=32.0, beta_slow=1.0,
+                   factors=None, stream=None)        frequencies: plain, linear, YaRN, per pair
+    qmm_rope(X, N, H, D, pos, freqs, rot, Y, layout=QMM_ROPE_HALF, mscale=1.0, x_stride=0,
+             y_stride=0, stream=None)                heads turned by their token's position
+    KvCache(k, v, dtype, pages, page, heads, dim)    a paged key-value cache (f16 or Q8_0 pools)
+    KvBatch(table, lens, seqs, max_pages, max_new, rows, starts=None, table_stride=0)
+                                                     a call's sequences and their new tokens
+    qmm_kv_append(cache, batch, K, V, freqs=None, rot=0, layout=QMM_ROPE_HALF, mscale=1.0,
+                  pos=None, k_norm=None, q_norm=None, eps=1e-5, Q=None, q_heads=0, q_out=None,
+                  q_stride=0, k_stride=0, v_stride=0, stream=None)
+                                                     keys (turned) and values into the cache,
+                                                     the queries turned beside them
 """
 from __future__ import annotations
 
@@ -61,13 +73,15 @@ QMM_ARGMAX_WORK_BYTES = 32768
 QMM_NOALLOC_SCRATCH_BYTES = 32768
 QMM_READ_PROBE_OUT_FLOATS = 4096
 QMM_ROUTE_SOFTMAX, QMM_ROUTE_SIGMOID = 0, 1
+QMM_F16 = 1
+QMM_ROPE_INTERLEAVED, QMM_ROPE_HALF = 0, 1
 QMM_MOE_MAX_EXPERTS, QMM_MOE_MAX_TOPK, QMM_MOE_MAX_ROWS, QMM_MOE_MAX_K = 1024, 32, 4194304, 1048576
 
 EXPORTS = ("qmm_gemv", "qmm_gemv_concat", "qmm_gemv_swiglu", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_gemm", "qmm_gemm_swiglu",
            "qmm_quantize_q8_0", "qmm_gemm_q8act", "qmm_gemv_q8act", "qmm_gemv_concat_q8act",
            "qmm_gemv_swiglu_q8act", "qmm_gemv_argmax_q8act", "qmm_repack_bytes", "qmm_repack", "qmm_gemm_repacked", "qmm_gemm_repacked_kernel",
            "qmm_block_norm", "qmm_moe_route", "qmm_moe_swiglu_work_bytes", "qmm_moe_swiglu", "qmm_moe_down_work_bytes",
-           "qmm_moe_down", "qmm_gemm_path", "qmm_gemm_q8act_path", "qmm_gemm_kernel", "qmm_gemm_swiglu_kernel", "qmm_read_probe", "qmm_blob_bytes", "qmm_block_elems",
+           "qmm_moe_down", "qmm_kv_pool_bytes", "qmm_rope", "qmm_rope_freqs", "qmm_kv_append", "qmm_gemm_path", "qmm_gemm_q8act_path", "qmm_gemm_kernel", "qmm_gemm_swiglu_kernel", "qmm_read_probe", "qmm_blob_bytes", "qmm_block_elems",
            "qmm_block_bytes", "qmm_strerror")
 
 _lib = None
@@ -143,6 +157,14 @@ def lib():
         L.qmm_moe_swiglu.restype = ci
         L.qmm_moe_down.argtypes = [vp, ci, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp]
         L.qmm_moe_down.restype = ci
+        L.qmm_kv_pool_bytes.argtypes = [ci, i64, i64, i64, i64]
+        L.qmm_kv_pool_bytes.restype = i64
+        L.qmm_rope.argtypes = [vp, i64, i64, i64, i64, vp, vp, i64, ci, f64, vp, i64, vp]
+        L.qmm_rope.restype = ci
+        L.qmm_rope_freqs.argtypes = [i64, f64, f64, f64, f64, f64, vp, vp, vp]
+        L.qmm_rope_freqs.restype = ci
+        L.qmm_kv_append.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, ci, f64, vp, vp, vp, f64, vp, i64, i64, vp, vp]
+        L.qmm_kv_append.restype = ci
         L.qmm_blob_bytes.argtypes = [ci, i64, i64]
         L.qmm_blob_bytes.restype = i64
         L.qmm_block_elems.argtypes = [ci]
@@ -468,3 +490,121 @@ def qmm_moe_down(w, dtype: int, E: int, M: int, K: int, N: int, T: int, ids, wei
                             _addr(Y, 4 * N * M, "Y", torch.float32), *_work(work), _stream(stream))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_moe_down")
+
+
+def _rows(t, rows: int, width: int, stride: int, what: str) -> int:
+    """Address of f32 rows of `width` values that lie `stride` values apart (0:
+    side by side).  The tensor may be a view into wider rows (columns of a fused
+    projection); what the rows reach must lie inside its storage."""
+    import torch
+    if t is None or isinstance(t, int):
+        return t or 0
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dtype is not torch.float32:
+        raise ValueError(f"{what} must be {torch.float32}, got {t.dtype}")
+    if not stride:
+        return _addr(t, 4 * rows * width, what, torch.float32)
+    if t.dim() and (t.stride(-1) != 1 or (t.dim() > 1 and t.shape[0] > 1 and t.stride(0) != stride)):
+        raise ValueError(f"{what} must have rows {stride} values apart")
+    if rows > 0 and width > 0:
+        held = t.untyped_storage().nbytes() // 4 - t.storage_offset()
+        if held < (rows - 1) * stride + width:
+            raise ValueError(f"{what} holds {held} values from its start, needs {(rows - 1) * stride + width}")
+    return t.data_ptr()
+
+
+def _on_current_device(*tensors) -> None:
+    """The kernels run on the current device: tensors of another are refused."""
+    import torch
+    at = None
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.is_cuda:
+            if at is None:
+                at = torch.cuda.current_device()
+            if t.device.index != at:
+                raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{at}")
+
+
+def kv_pool_bytes(dtype: int, pages: int, page: int, heads: int, dim: int) -> int:
+    """Bytes of the key pool, and of the value pool, of a paged cache."""
+    return lib().qmm_kv_pool_bytes(dtype, pages, page, heads, dim)
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class _KvBatchStruct(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("max_new", ctypes.c_int64), ("rows", ctypes.c_int64)]
+
+
+class KvCache:
+    """A paged key-value cache: two device pools of kv_pool_bytes(...) bytes
+    (any tensor type), described for the calls that take it (qmm_kv_cache)."""
+
+    def __init__(self, k, v, dtype: int, pages: int, page: int, heads: int, dim: int):
+        need = kv_pool_bytes(dtype, pages, page, heads, dim) or None
+        self.k, self.v = k, v
+        self.dtype, self.pages, self.page, self.heads, self.dim = dtype, pages, page, heads, dim
+        self.struct = _KvCacheStruct(_addr(k, need, "k"), _addr(v, need, "v"), pages, dtype, page, heads, dim)
+        self.ref = ctypes.addressof(self.struct)
+
+
+class KvBatch:
+    """The sequences of a call and their new tokens (qmm_kv_batch): the page
+    table int32 [seqs][table_stride], lens int32 [seqs], starts int32 [seqs + 1] or
+    None.  The tensors may change between calls; they are read on the device."""
+
+    def __init__(self, table, lens, seqs: int, max_pages: int, max_new: int, rows: int, starts=None,
+                 table_stride: int = 0):
+        import torch
+        i32 = torch.int32
+        self.table, self.lens, self.starts = table, lens, starts
+        self.seqs, self.max_pages, self.max_new, self.rows = seqs, max_pages, max_new, rows
+        wide = (seqs - 1) * (table_stride or max_pages) + max_pages
+        self.struct = _KvBatchStruct(_addr(table, 4 * wide, "table", i32), _addr(lens, 4 * seqs, "lens", i32),
+                                     _addr(starts, 4 * (seqs + 1), "starts", i32), seqs, max_pages, table_stride, max_new,
+                                     rows)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def qmm_rope_freqs(rot: int, base: float, freqs, factor: float = 1.0, context: float = 0.0, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0, factors=None, stream=None) -> None:
+    import torch
+    _on_current_device(freqs, factors)
+    rc = lib().qmm_rope_freqs(rot, base, factor, context, beta_fast, beta_slow,
+                              _addr(factors, 2 * rot, "factors", torch.float32),
+                              _addr(freqs, 2 * rot, "freqs", torch.float32), _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_rope_freqs")
+
+
+def qmm_rope(X, N: int, H: int, D: int, pos, freqs, rot: int, Y, layout: int = QMM_ROPE_HALF, mscale: float = 1.0,
+             x_stride: int = 0, y_stride: int = 0, stream=None) -> None:
+    import torch
+    _on_current_device(X, pos, freqs, Y)
+    rc = lib().qmm_rope(_rows(X, N, H * D, x_stride, "X"), x_stride, N, H, D, _addr(pos, 4 * N, "pos", torch.int32),
+                        _addr(freqs, 2 * rot, "freqs", torch.float32), rot, layout, mscale,
+                        _rows(Y, N, H * D, y_stride, "Y"), y_stride, _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_rope")
+
+
+def qmm_kv_append(cache: KvCache, batch: KvBatch, K, V, freqs=None, rot: int = 0, layout: int = QMM_ROPE_HALF,
+                  mscale: float = 1.0, pos=None, k_norm=None, q_norm=None, eps: float = 1e-5, Q=None, q_heads: int = 0,
+                  q_out=None, q_stride: int = 0, k_stride: int = 0, v_stride: int = 0, stream=None) -> None:
+    import torch
+    f32, D, rows = torch.float32, cache.dim, batch.rows
+    _on_current_device(cache.k, cache.v, batch.table, batch.lens, batch.starts, K, V, freqs, pos, k_norm, q_norm, Q, q_out)
+    rc = lib().qmm_kv_append(cache.ref, batch.ref, _rows(K, rows, cache.heads * D, k_stride, "K"), k_stride,
+                             _rows(V, rows, cache.heads * D, v_stride, "V"), v_stride, _addr(freqs, 2 * rot, "freqs", f32),
+                             rot, layout, mscale, _addr(pos, 4 * rows, "pos", torch.int32),
+                             _addr(k_norm, 4 * D, "k_norm", f32), _addr(q_norm, 4 * D, "q_norm", f32), eps,
+                             _rows(Q, rows, q_heads * D, q_stride, "Q"), q_stride, q_heads,
+                             _addr(q_out, 4 * rows * q_heads * D, "q_out", f32), _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_kv_append")

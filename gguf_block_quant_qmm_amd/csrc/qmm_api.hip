@@ -168,6 +168,42 @@ int check_work(const void *work, int64_t work_bytes, int64_t need) {
     return work_bytes < need ? QMM_ERR_SCRATCH : QMM_OK;
 }
 
+// A paged cache and the sequences of a call (qmm_kv_cache, qmm_kv_batch).
+bool kv_sizes_ok(int64_t pages, int64_t page, int64_t heads, int64_t dim) {
+    if (pages < 1 || pages > INT32_MAX || heads < 1 || heads > 1024) return false;
+    if (page < 16 || page > 1024 || (page & (page - 1)) != 0) return false;
+    return dim == 64 || dim == 96 || dim == 128 || dim == 192 || dim == 256;
+}
+
+int64_t kv_pool_bytes(int dtype, int64_t pages, int64_t page, int64_t heads, int64_t dim) {
+    return pages * heads * (dtype == QMM_F16 ? 2 * page * dim : page * dim + page * dim / 16);
+}
+
+int check_kv(const qmm_kv_cache *c, const qmm_kv_batch *b) {
+    if (!c || !b) return QMM_ERR_NULL;
+    if (c->dtype != QMM_F16 && c->dtype != QMM_Q8_0) return QMM_ERR_DTYPE;
+    if (!kv_sizes_ok(c->pages, c->page, c->heads, c->dim)) return QMM_ERR_SHAPE;
+    if (b->seqs < 1 || b->seqs > 65535 || b->max_new < 1 || b->max_new > INT32_MAX / b->seqs) return QMM_ERR_SHAPE;
+    if (b->rows < 1 || b->rows > INT32_MAX || (!b->starts && b->rows < b->seqs * b->max_new)) return QMM_ERR_SHAPE;
+    if (b->max_pages < 1 || b->max_pages > INT32_MAX / c->page) return QMM_ERR_SHAPE;
+    if (b->table_stride != 0 && (b->table_stride < b->max_pages || b->table_stride > (int64_t(1) << 40)))
+        return QMM_ERR_SHAPE;
+    return QMM_OK;
+}
+
+int check_kv_pointers(const qmm_kv_cache &c, const qmm_kv_batch &b) {
+    if (!c.k || !c.v || !b.table || !b.lens) return QMM_ERR_NULL;
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(b.table, 4) || !aligned(b.lens, 4) || !aligned(b.starts, 4))
+        return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+// A row stride in floats (0: the row's `width` values, side by side), or -1.
+int64_t row_stride(int64_t stride, int64_t width) {
+    if (stride == 0) return width;
+    return stride >= width && stride % 4 == 0 && stride <= (int64_t(1) << 40) ? stride : -1;
+}
+
 }  // namespace
 
 extern "C" {
@@ -583,6 +619,78 @@ int qmm_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int6
     if (rc != QMM_OK) return rc;
     const hipError_t e = qmm::launch_moe_down(w, dtype, E, M, K, N, T, ids, weights, H, residual, Y, work,
                                               (hipStream_t)stream, cus);
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int64_t qmm_kv_pool_bytes(int dtype, int64_t pages, int64_t page, int64_t heads, int64_t dim) {
+    if ((dtype != QMM_F16 && dtype != QMM_Q8_0) || !kv_sizes_ok(pages, page, heads, dim)) return 0;
+    return kv_pool_bytes(dtype, pages, page, heads, dim);
+}
+
+int qmm_rope(const float *X, int64_t x_stride, int64_t N, int64_t H, int64_t D, const int32_t *pos, const float *freqs,
+             int64_t rot, int layout, double mscale, float *Y, int64_t y_stride, void *stream) {
+    if (N < 1 || N > INT32_MAX || H < 1 || H > 65536 || D < 8 || D > 1024 || D % 8 != 0) return QMM_ERR_SHAPE;
+    if (rot < 8 || rot > D || rot % 8 != 0) return QMM_ERR_SHAPE;
+    const int64_t xs = row_stride(x_stride, H * D), ys = row_stride(y_stride, H * D);
+    if (xs < 0 || ys < 0) return QMM_ERR_SHAPE;
+    if ((layout != QMM_ROPE_INTERLEAVED && layout != QMM_ROPE_HALF) || !std::isfinite(mscale)) return QMM_ERR_VALUE;
+    if (!X || !pos || !freqs || !Y) return QMM_ERR_NULL;
+    if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(pos, 4) || !aligned(freqs, 4)) return QMM_ERR_ALIGN;
+    int cus = 0;
+    const int rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e = qmm::launch_rope(X, xs, N, H, D, pos, freqs, rot, layout == QMM_ROPE_HALF, mscale, Y, ys,
+                                          (hipStream_t)stream);
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int qmm_rope_freqs(int64_t rot, double base, double factor, double context, double beta_fast, double beta_slow,
+                   const float *factors, float *freqs, void *stream) {
+    if (rot < 2 || rot > 1024 || rot % 2 != 0) return QMM_ERR_SHAPE;
+    for (const double v : {base, factor, context, beta_fast, beta_slow})
+        if (!std::isfinite(v)) return QMM_ERR_VALUE;
+    if (base <= 1.0 || factor <= 0.0 || context < 0.0 || beta_slow <= 0.0 || beta_fast <= beta_slow) return QMM_ERR_VALUE;
+    if (!freqs) return QMM_ERR_NULL;
+    if (!aligned(factors, 4) || !aligned(freqs, 4)) return QMM_ERR_ALIGN;
+    int cus = 0;
+    const int rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e =
+        qmm::launch_rope_freqs(rot, base, factor, context, beta_fast, beta_slow, factors, freqs, (hipStream_t)stream);
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const float *K, int64_t k_stride, const float *V,
+                  int64_t v_stride, const float *freqs, int64_t rot, int layout, double mscale, const int32_t *pos,
+                  const float *k_norm, const float *q_norm, double eps, const float *Q, int64_t q_stride, int64_t q_heads,
+                  float *q_out, void *stream) {
+    int rc = check_kv(cache, batch);
+    if (rc != QMM_OK) return rc;
+    const int64_t D = cache->dim, ks = row_stride(k_stride, cache->heads * D), vs = row_stride(v_stride, cache->heads * D);
+    if (ks < 0 || vs < 0) return QMM_ERR_SHAPE;
+    if (freqs && (rot < 8 || rot > D || rot % 8 != 0)) return QMM_ERR_SHAPE;
+    int64_t qs = 0;
+    if (Q) {
+        if (q_heads < 1 || q_heads > 65536) return QMM_ERR_SHAPE;
+        qs = row_stride(q_stride, q_heads * D);
+        if (qs < 0) return QMM_ERR_SHAPE;
+    }
+    if (freqs && ((layout != QMM_ROPE_INTERLEAVED && layout != QMM_ROPE_HALF) || !std::isfinite(mscale)))
+        return QMM_ERR_VALUE;
+    if (!std::isfinite(eps) || eps < 0.0) return QMM_ERR_VALUE;
+    if (!K || !V || (!Q != !q_out)) return QMM_ERR_NULL;
+    rc = check_kv_pointers(*cache, *batch);
+    if (rc != QMM_OK) return rc;
+    for (const void *p : {(const void *)K, (const void *)V, (const void *)Q, (const void *)q_out, (const void *)k_norm,
+                          (const void *)q_norm})
+        if (!aligned(p, 16)) return QMM_ERR_ALIGN;
+    if (!aligned(freqs, 4) || !aligned(pos, 4)) return QMM_ERR_ALIGN;
+    int cus = 0;
+    rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e =
+        qmm::launch_kv_append(*cache, *batch, K, ks, V, vs, freqs, rot, layout == QMM_ROPE_HALF, mscale, pos, k_norm,
+                              q_norm, eps, Q, qs, q_heads, q_out, (hipStream_t)stream);
     return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 

@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include "qmm.h"
+
 namespace qmm {
 
 // Tuning levers.  A measurement build (compiled with -DQMM_TUNING) reads
@@ -105,6 +107,20 @@ hipError_t launch_gemm_q8act_mfma(int dtype, const void *blob, int64_t M, int64_
 // Needs gemv_fused_ok(dtype, K).
 hipError_t launch_gemv_q8in(int mode, int n, const void *const *blobs, const int64_t *Ms, int dtype, int64_t K,
                             const float *x, float *const *ys, hipStream_t st, int cus);
+
+// Rotary positions (qmm_rope.hip): D and rot multiples of 8, rot <= D <= 1024.
+hipError_t launch_rope(const float *X, int64_t x_stride, int64_t N, int64_t H, int64_t D, const int32_t *pos,
+                       const float *freqs, int64_t rot, bool half, double mscale, float *Y, int64_t y_stride,
+                       hipStream_t st);
+hipError_t launch_rope_freqs(int64_t rot, double base, double factor, double context, double fast, double slow,
+                             const float *factors, float *freqs, hipStream_t st);
+
+// New keys (normed, turned), values and turned queries (qmm_rope.hip); freqs,
+// pos, the norms and Q with q_out may be NULL as qmm_kv_append allows.
+hipError_t launch_kv_append(const qmm_kv_cache &cache, const qmm_kv_batch &batch, const float *K, int64_t k_stride,
+                            const float *V, int64_t v_stride, const float *freqs, int64_t rot, bool half, double mscale,
+                            const int32_t *pos, const float *k_norm, const float *q_norm, double eps, const float *Q,
+                            int64_t q_stride, int64_t q_heads, float *q_out, hipStream_t st);
 
 // The norms after and before a block with its gate and residual scale
 // (qmm_norm.hip): K <= 2^28, block / w_post / gate / residual_out / w_pre / H /

@@ -76,7 +76,7 @@ extern "C" {
 /* status codes */
 #define QMM_OK 0
 #define QMM_ERR_NULL (-1)    /* a required pointer is NULL                          */
-#define QMM_ERR_DTYPE (-2)   /* dtype is not one of the six tags above              */
+#define QMM_ERR_DTYPE (-2)   /* dtype is not one that the call takes               */
 #define QMM_ERR_SHAPE (-3)   /* M < 1, N < 1, K < block_elems or K % block_elems,
                                 a size above 2^40 or a product of two above 2^56   */
 #define QMM_ERR_ALIGN (-4)   /* blob not 16-B aligned, x/X not 16-B, y/Y not 4-B    */
@@ -451,6 +451,124 @@ int64_t qmm_moe_down_work_bytes(int dtype, int64_t E, int64_t M, int64_t K, int6
 int qmm_moe_down(const void *w, int dtype, int64_t E, int64_t M, int64_t K, int64_t N, int64_t T, const int32_t *ids,
                  const float *weights, const float *H, const float *residual, float *Y, void *work, int64_t work_bytes,
                  void *stream);
+
+/* ---- the attention half of a decoder layer over a paged key-value cache ----
+ *
+ * A cache (one per layer) is two pools, keys and values, of `pages` pages.  A
+ * page holds `page` tokens of all `heads` key-value heads.  In a pool, page p
+ * of head h is the record p * heads + h of qmm_kv_pool_bytes(dtype, 1, page, 1,
+ * dim) bytes:
+ *     QMM_F16   keys f16 [page][dim];  values f16 [dim][page]
+ *     QMM_Q8_0  keys int8 [page][dim], then their scales f16 [dim/32][page];
+ *               values int8 [dim][page], then their scales f16 [dim/32][page]
+ *               (a Q8_0 block is 32 neighbouring dims of one token and head, as
+ *               qmm_quantize_q8_0 makes it: the same codes and scales)
+ * Values lie with the token index inside, the order in which the matrix cores
+ * take them.
+ *   k, v    device pools, 16-B aligned, qmm_kv_pool_bytes(...) bytes each
+ *   dtype   QMM_F16 or QMM_Q8_0, else QMM_ERR_DTYPE
+ *   page    16, 32, 64, 128, 256, 512 or 1024; dim 64, 96, 128, 192 or 256;
+ *           1 <= heads <= 1024, 1 <= pages <= 2^31 - 1: else QMM_ERR_SHAPE */
+#define QMM_F16 1
+typedef struct qmm_kv_cache {
+    void *k, *v;
+    int64_t pages;
+    int32_t dtype, page, heads, dim;
+} qmm_kv_cache;
+
+/* The sequences of one call and their new tokens.  Sequence s has lens[s]
+ * tokens, its n_s new ones (those of this call) included and last: new token t
+ * is token lens[s] - n_s + t of its sequence (its index).  Token i lies in page
+ * table[s * table_stride + i / page], at i % page.
+ *   table   device int32 [seqs][table_stride], 4-B aligned; columns 0 ..
+ *           max_pages - 1 are looked at (table_stride 0: max_pages)
+ *   lens    device int32 [seqs], 4-B aligned
+ *   starts  device int32 [seqs + 1], 4-B aligned, not falling: the new tokens of s are the rows
+ *           starts[s] .. starts[s+1] - 1 of the call's arrays (none, or up to
+ *           max_new); or NULL: every sequence has max_new, s's from row s * max_new
+ *   rows    rows of the call's arrays.  With starts, rows outside all sequences
+ *           (padding) are neither read nor written; without,
+ *           rows >= seqs * max_new
+ * The arrays stay on the device: the same call can be captured once and replayed
+ * while they change.  What they may hold: a token without a page (an index
+ * below 0 or at max_pages * page or more, or a page id outside 0 .. pages-1) is
+ * no token: it is not stored, and attention does not see it.  1 <= seqs, max_new,
+ * max_pages, rows; seqs * max_new, rows and max_pages * page at most 2^31 - 1, seqs at
+ * most 65535; max_pages <= table_stride: else QMM_ERR_SHAPE.  A sequence with
+ * more than max_new rows in starts: its rows from max_new on are left alone.
+ * The structs are read before a call returns and not kept. */
+typedef struct qmm_kv_batch {
+    const int32_t *table, *lens, *starts;
+    int64_t seqs, max_pages, table_stride, max_new, rows;
+} qmm_kv_batch;
+
+/* Bytes of one pool; 0 if dtype or a size is invalid. */
+int64_t qmm_kv_pool_bytes(int dtype, int64_t pages, int64_t page, int64_t heads, int64_t dim);
+
+/* Rotary positions.  A head's first rot values are turned in pairs, the others
+ * pass: pair i of a token at position pos has the angle a = pos * freqs[i], and
+ *     (u, w) -> mscale * (u cos a - w sin a,  u sin a + w cos a)
+ *     QMM_ROPE_INTERLEAVED  pair i is values 2i and 2i + 1
+ *     QMM_ROPE_HALF         pair i is values i and rot/2 + i
+ * in f64, angles too; rounded to f32 once.  A negative position turns back
+ * (the inverse, and with mscale 1 the gradient, of the positive one).
+ *   X       device f32, token n's H heads of D values at X + n * x_stride, 16-B
+ *           aligned; x_stride >= H * D, a multiple of 4 (0: H * D)
+ *   pos     device int32 [N], 4-B aligned
+ *   freqs   device f32 [rot/2], 4-B aligned, as qmm_rope_freqs makes them
+ *   Y       device f32, as X with y_stride; overwritten; may be X itself
+ *           where y_stride = x_stride, else it overlaps nothing
+ * D and rot multiples of 8, 8 <= rot <= D <= 1024, 1 <= H <= 2^16, 1 <= N <=
+ * 2^31 - 1: else QMM_ERR_SHAPE.  mscale finite, layout known: else
+ * QMM_ERR_VALUE. */
+#define QMM_ROPE_INTERLEAVED 0
+#define QMM_ROPE_HALF 1
+int qmm_rope(const float *X, int64_t x_stride, int64_t N, int64_t H, int64_t D, const int32_t *pos, const float *freqs,
+             int64_t rot, int layout, double mscale, float *Y, int64_t y_stride, void *stream);
+
+/* The frequencies of rot/2 pairs, in f64, rounded to f32 once (computed when a
+ * model is loaded).  f_i = base^(-2i/rot); then f_i / factors[i] (a GGUF
+ * model's rope_freqs tensor) where given; then
+ *     context 0: f_i / factor (linear scaling; factor 1: none)
+ *     context c, YaRN: pairs that turn more than beta_fast times over the c
+ *     tokens of training keep f_i, pairs below beta_slow turns have f_i / factor, those
+ *     between are mixed: with r(b) = rot ln(c / (2 pi b)) / (2 ln base), low =
+ *     max(floor r(beta_fast), 0), high = min(ceil r(beta_slow), rot - 1) and
+ *     g = (i - low) / max(high - low, 0.001) cut to 0 .. 1:
+ *     f_i (1 - g) + f_i / factor * g.
+ * YaRN's mscale for qmm_rope is 0.1 ln(factor) + 1.
+ *   factors device f32 [rot/2] or NULL, freqs device f32 [rot/2]; 4-B aligned
+ * rot even, 2 <= rot <= 1024: else QMM_ERR_SHAPE.  base > 1, factor > 0, context
+ * >= 0, 0 < beta_slow < beta_fast, all finite: else QMM_ERR_VALUE. */
+int qmm_rope_freqs(int64_t rot, double base, double factor, double context, double beta_fast, double beta_slow,
+                   const float *factors, float *freqs, void *stream);
+
+/* The new tokens' keys and values into the cache, the keys turned on the way,
+ * and the queries turned beside them, in one launch (page "cera 0.3.1
+ * src/model/gpu_lfm2.rs": the batched q/k norm + rope).  Per row n of a sequence:
+ *     key    = turn(norm(K[n][h], k_norm)) as f32, stored as dtype
+ *     value  = V[n][h], stored as dtype
+ *     q_out[n][h] = turn(norm(Q[n][h], q_norm))
+ * turn is qmm_rope's at the token's index (or pos[n]); norm(x, w) = x /
+ * sqrt(mean(x^2) + eps) * w over the head's values, or x where w is NULL; all in
+ * f64, rounded to f32 once, then to f16 (nearest even, beyond 65504 infinite)
+ * or to a Q8_0 block.
+ *   K, V    device f32, row n's heads at K + n * k_stride, V + n * v_stride;
+ *           16-B aligned; strides as x_stride above (0: heads * dim)
+ *   freqs   as for qmm_rope, or NULL: nothing is turned (rot, layout, mscale and
+ *           pos are then ignored).  rot a multiple of 8, 8 <= rot <= dim
+ *   pos     device int32 [rows] or NULL: the token's index
+ *   k_norm, q_norm  device f32 [dim], 16-B aligned, or NULL;  eps finite, >= 0
+ *   Q, q_out  device f32, q_heads heads of dim values a row, Q + n * q_stride
+ *           (0: q_heads * dim) and q_out [rows][q_heads * dim], 16-B aligned, or
+ *           both NULL.  q_out may be Q itself where the rows lie the same
+ * Rows of padding leave q_out as it is.  A token without a page still has its
+ * queries turned (its index may be negative).  Two tokens of a call must not share a place in the cache.
+ * 1 <= q_heads <= 2^16 with Q. */
+int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const float *K, int64_t k_stride, const float *V,
+                  int64_t v_stride, const float *freqs, int64_t rot, int layout, double mscale, const int32_t *pos,
+                  const float *k_norm, const float *q_norm, double eps, const float *Q, int64_t q_stride, int64_t q_heads,
+                  float *q_out, void *stream);
 
 /* Which arithmetic qmm_gemm uses for these sizes: 0 = f32 (GEMV family),
  * 1 = f16 matrix-core GEMM, or a negative status for invalid arguments. */
