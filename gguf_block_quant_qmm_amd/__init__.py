@@ -52,6 +52,9 @@ there is no CPU fallback.
                   q_stride=0, k_stride=0, v_stride=0, stream=None)
                                                      keys (turned) and values into the cache,
                                                      the queries turned beside them
+    qmm_attention(cache, batch, Q, q_heads, out, scale=None, causal=True, window=0, softcap=0.0,
+                  work=None, q_stride=0, stream=None)
+                                                     the new tokens' attention over the cache
 """
 from __future__ import annotations
 
@@ -81,7 +84,8 @@ EXPORTS = ("qmm_gemv", "qmm_gemv_concat", "qmm_gemv_swiglu", "qmm_gemv_argmax", 
            "qmm_quantize_q8_0", "qmm_gemm_q8act", "qmm_gemv_q8act", "qmm_gemv_concat_q8act",
            "qmm_gemv_swiglu_q8act", "qmm_gemv_argmax_q8act", "qmm_repack_bytes", "qmm_repack", "qmm_gemm_repacked", "qmm_gemm_repacked_kernel",
            "qmm_block_norm", "qmm_moe_route", "qmm_moe_swiglu_work_bytes", "qmm_moe_swiglu", "qmm_moe_down_work_bytes",
-           "qmm_moe_down", "qmm_kv_pool_bytes", "qmm_rope", "qmm_rope_freqs", "qmm_kv_append", "qmm_gemm_path", "qmm_gemm_q8act_path", "qmm_gemm_kernel", "qmm_gemm_swiglu_kernel", "qmm_read_probe", "qmm_blob_bytes", "qmm_block_elems",
+           "qmm_moe_down", "qmm_kv_pool_bytes", "qmm_rope", "qmm_rope_freqs", "qmm_kv_append",
+           "qmm_attention_work_bytes", "qmm_attention", "qmm_gemm_path", "qmm_gemm_q8act_path", "qmm_gemm_kernel", "qmm_gemm_swiglu_kernel", "qmm_read_probe", "qmm_blob_bytes", "qmm_block_elems",
            "qmm_block_bytes", "qmm_strerror")
 
 _lib = None
@@ -165,6 +169,10 @@ def lib():
         L.qmm_rope_freqs.restype = ci
         L.qmm_kv_append.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, ci, f64, vp, vp, vp, f64, vp, i64, i64, vp, vp]
         L.qmm_kv_append.restype = ci
+        L.qmm_attention_work_bytes.argtypes = [vp, vp, i64]
+        L.qmm_attention_work_bytes.restype = i64
+        L.qmm_attention.argtypes = [vp, vp, vp, i64, i64, f64, ci, i64, f64, vp, vp, i64, vp]
+        L.qmm_attention.restype = ci
         L.qmm_blob_bytes.argtypes = [ci, i64, i64]
         L.qmm_blob_bytes.restype = i64
         L.qmm_block_elems.argtypes = [ci]
@@ -608,3 +616,21 @@ def qmm_kv_append(cache: KvCache, batch: KvBatch, K, V, freqs=None, rot: int = 0
                              _addr(q_out, 4 * rows * q_heads * D, "q_out", f32), _stream(stream))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_kv_append")
+
+
+def attention_work_bytes(cache: KvCache, batch: KvBatch, q_heads: int) -> int:
+    """Bytes of work that qmm_attention needs for these sizes (0: none)."""
+    return lib().qmm_attention_work_bytes(cache.ref, batch.ref, q_heads)
+
+
+def qmm_attention(cache: KvCache, batch: KvBatch, Q, q_heads: int, out, scale: float | None = None, causal: bool = True,
+                  window: int = 0, softcap: float = 0.0, work=None, q_stride: int = 0, stream=None) -> None:
+    """scale None: 1 / sqrt(dim)."""
+    import torch
+    D, rows = cache.dim, batch.rows
+    _on_current_device(cache.k, cache.v, batch.table, batch.lens, batch.starts, Q, out, work)
+    rc = lib().qmm_attention(cache.ref, batch.ref, _rows(Q, rows, q_heads * D, q_stride, "Q"), q_stride, q_heads,
+                             D ** -0.5 if scale is None else scale, int(bool(causal)), window, softcap,
+                             _addr(out, 4 * rows * q_heads * D, "out", torch.float32), *_work(work), _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_attention")

@@ -198,6 +198,15 @@ int check_kv_pointers(const qmm_kv_cache &c, const qmm_kv_batch &b) {
     return QMM_OK;
 }
 
+int check_attention(const qmm_kv_cache *c, const qmm_kv_batch *b, int64_t q_heads) {
+    const int rc = check_kv(c, b);
+    if (rc != QMM_OK) return rc;
+    if (q_heads < c->heads || q_heads > 65536 || q_heads % c->heads != 0) return QMM_ERR_SHAPE;
+    // a sequence's query rows of one key-value head are counted in 31 bits, as are the units
+    if (b->max_new > INT32_MAX / (q_heads / c->heads) || b->seqs * c->heads > INT32_MAX) return QMM_ERR_SHAPE;
+    return QMM_OK;
+}
+
 // A row stride in floats (0: the row's `width` values, side by side), or -1.
 int64_t row_stride(int64_t stride, int64_t width) {
     if (stride == 0) return width;
@@ -691,6 +700,34 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
     const hipError_t e =
         qmm::launch_kv_append(*cache, *batch, K, ks, V, vs, freqs, rot, layout == QMM_ROPE_HALF, mscale, pos, k_norm,
                               q_norm, eps, Q, qs, q_heads, q_out, (hipStream_t)stream);
+    return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+int64_t qmm_attention_work_bytes(const qmm_kv_cache *cache, const qmm_kv_batch *batch, int64_t q_heads) {
+    return check_attention(cache, batch, q_heads) == QMM_OK ? qmm::attention_work_bytes(*cache, *batch, q_heads) : 0;
+}
+
+int qmm_attention(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const float *Q, int64_t q_stride, int64_t q_heads,
+                  double scale, int causal, int64_t window, double softcap, float *out, void *work, int64_t work_bytes,
+                  void *stream) {
+    int rc = check_attention(cache, batch, q_heads);
+    if (rc != QMM_OK) return rc;
+    const int64_t qs = row_stride(q_stride, q_heads * cache->dim);
+    if (qs < 0) return QMM_ERR_SHAPE;
+    if (!std::isfinite((float)scale) || !std::isfinite((float)softcap) || softcap < 0.0 || window < 0 ||
+        (window > 0 && !causal) || window > (int64_t(1) << 40))
+        return QMM_ERR_VALUE;
+    if (!Q || !out) return QMM_ERR_NULL;
+    rc = check_kv_pointers(*cache, *batch);
+    if (rc != QMM_OK) return rc;
+    if (!aligned(Q, 16) || !aligned(out, 16)) return QMM_ERR_ALIGN;
+    rc = check_work(work, work_bytes, qmm::attention_work_bytes(*cache, *batch, q_heads));
+    if (rc != QMM_OK) return rc;
+    int cus = 0;
+    rc = current_device(&cus);
+    if (rc != QMM_OK) return rc;
+    const hipError_t e = qmm::launch_attention(*cache, *batch, Q, qs, q_heads, scale, causal != 0, window, softcap, out,
+                                               work, (hipStream_t)stream);
     return e == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 

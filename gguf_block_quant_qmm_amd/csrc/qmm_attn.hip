@@ -1,0 +1,570 @@
+// qmm_attn.hip -- attention of a few new tokens over the paged cache (one
+// decoded token, drafted tokens; include/qmm.h, qmm_attention), and the join of
+// what several workgroups made of one row.
+//
+// Per row:  x_j = scale q . k_j,  out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m)
+// (x in base 2, m its running maximum), one pass over the row's tokens.
+//
+// Bound by memory: every key and value is read once for all G query heads of its
+// head and all new tokens.  The matrix cores do the products, because a row of f32
+// FMAs would cost as many instructions per query head as there are bytes:
+//   scores^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens' keys (a lane's 8
+//                      values are 16 bytes of its token's key), B = 16 columns of
+//                      queries
+//   out^T   += V^T P^T A = 16 dims of the values (the pool holds them with the
+//                      token inside: a lane's 8 tokens are 16 bytes), B = the
+//                      probabilities, which the first product leaves in the lane
+//                      that needs them: token 8 g + 4 t + i of a chunk of 32 is row
+//                      4 g + i of product t, so lane (column, g) holds its 8 tokens
+// f32 class: queries (under a power of two) and probabilities (times 2^15) are split
+// in two f16 parts.  Up to 8 rows (G heads, one token) both parts sit in one
+// tile's columns 0-7 and 8-15, at the price of one; more rows take two
+// products.  Q8_0: a step of 32 dims is one block, so its product of codes is
+// scaled by the token's key scale in f32; the value scale goes into the
+// probability, under a running power of two as the maximum is.
+//
+// No LDS on the way in: a wavefront holds 32 tokens of keys and values in
+// registers and asks for the next chunk's keys as soon as the scores are done, the
+// next values after the second product.  The four wavefronts of a workgroup take
+// every fourth chunk and join through LDS; workgroups that share a row write their
+// sums and maxima to `work`, joined by a second launch.
+#include <type_traits>
+
+#include "qmm_attn.hpp"
+
+namespace qmm {
+
+namespace {
+
+constexpr int kWaves = 4, kChunk = 32, kLeast = 4;
+
+template <int D, bool Q8> struct Regs;  // keys and values of a chunk
+template <int D> struct Regs<D, false> {
+    u32x4_t k[2][D / 32], v[D / 16];
+};
+template <int D> struct Regs<D, true> {
+    u32x2_t k[2][D / 32], v[D / 16];
+    half8 ks[D / 32], vs[D / 32];  // scales of tokens 8g .. 8g+7
+};
+
+// Where a lane's tokens of a chunk lie: the token whose key it loads is in group
+// r / 4 of 8 (r = lane % 16), its values' and scores' tokens are group g = lane / 16.
+struct Where {
+    const uint8_t *k;   // record with the keys
+    const uint8_t *ks;  // record with the scales of group g's keys (Q8_0)
+    const uint8_t *v;   // record with the values of group g
+    int kslot, slot;
+    bool good;          // group g has a page
+};
+
+template <bool Q8>
+__device__ __forceinline__ Where where(const AttnArgs &a, int s, int h, int64_t k0, int64_t rec) {
+    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int64_t kk = k0 + 8 * (r >> 2), kv = k0 + 8 * g;
+    const int pk = kv_page(a.kv, s, kk), pv = kv_page(a.kv, s, kv);
+    const int mask = (1 << a.kv.page_shift) - 1;
+    Where w;
+    w.good = pv >= 0;
+    // a group without a page reads page 0 and is masked
+    const int64_t ok = ((int64_t)(pk < 0 ? 0 : pk) * a.kv.heads + h) * rec, ov = ((int64_t)(pv < 0 ? 0 : pv) * a.kv.heads + h) * rec;
+    w.k = a.kv.k + ok;
+    w.ks = a.kv.k + ov;
+    w.v = a.kv.v + ov;
+    w.kslot = ((int)kk & mask) + (r & 3);
+    w.slot = (int)kv & mask;
+    return w;
+}
+
+template <int D, bool Q8>
+__device__ __forceinline__ void load_keys(const AttnArgs &a, const Where &w, Regs<D, Q8> &x) {
+    const int g = ((int)threadIdx.x & 63) >> 4, page = 1 << a.kv.page_shift;
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int b = 0; b < D / 32; b++) {
+            const int at = (w.kslot + 4 * t) * D + 32 * b + 8 * g;
+            if constexpr (Q8) x.k[t][b] = *reinterpret_cast<const u32x2_t *>(w.k + at);
+            else x.k[t][b] = *reinterpret_cast<const u32x4_t *>(w.k + 2 * at);
+        }
+    if constexpr (Q8) {
+#pragma unroll
+        for (int b = 0; b < D / 32; b++)
+            x.ks[b] = *reinterpret_cast<const half8 *>(w.ks + page * D + 2 * (b * page + w.slot));
+    }
+}
+
+template <int D, bool Q8>
+__device__ __forceinline__ void load_values(const AttnArgs &a, const Where &w, Regs<D, Q8> &x) {
+    const int r = (int)threadIdx.x & 15, page = 1 << a.kv.page_shift;
+#pragma unroll
+    for (int d = 0; d < D / 16; d++) {
+        const int at = (16 * d + r) * page + w.slot;
+        if constexpr (Q8) x.v[d] = *reinterpret_cast<const u32x2_t *>(w.v + at);
+        else x.v[d] = *reinterpret_cast<const u32x4_t *>(w.v + 2 * at);
+    }
+    if constexpr (Q8) {
+#pragma unroll
+        for (int b = 0; b < D / 32; b++)
+            x.vs[b] = *reinterpret_cast<const half8 *>(w.v + page * D + 2 * (b * page + w.slot));
+    }
+}
+
+// MODE 0: up to 8 rows a workgroup, both parts in one column tile; 1, 2: one or
+// two tiles of 16 rows, each part its own product.
+template <int D, bool Q8, int MODE>
+__global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel(const AttnArgs a) {
+    constexpr int NC = MODE == 0 ? 1 : MODE, RT = MODE == 0 ? 8 : 16 * MODE, NK = D / 32, ND = D / 16;
+    constexpr bool STACK = MODE == 0;
+    __shared__ __attribute__((aligned(16))) float lo_[kWaves][16][D + 4];
+    __shared__ float2 lstat[kWaves][NC * 16];
+    AttnShare w;
+    if (!attn_share<RT, kChunk>(a, kLeast, w)) return;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int64_t rec = kv_record(Q8 ? QMM_Q8_0 : QMM_F16, (int64_t)1 << a.kv.page_shift, D);
+
+    // the queries' two parts, and what each of the lane's columns sees
+    half8 qh[NC][NK], ql[NC][NK];
+    float mul[NC];
+    int64_t lo[NC], hi[NC];
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+        const int r = STACK ? (col & 7) : 16 * c + col;
+        const bool on = r < w.nrows;
+        const int row = w.r0 + (on ? r : 0), t = row / a.G, hq = w.h * a.G + (row - t * a.G);
+        attn_sees(a, w.nw, t, lo[c], hi[c]);
+        if (!on) lo[c] = hi[c] = 0;
+        const float *q = a.Q + (int64_t)(w.nw.first + t) * a.q_stride + (int64_t)hq * D + 8 * g;
+        floatx4 x[NK][2];
+        float amax = 0.f;
+#pragma unroll
+        for (int b = 0; b < NK; b++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                x[b][i] = *reinterpret_cast<const floatx4 *>(q + 32 * b + 4 * i);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    if (!on) x[b][i][j] = 0.f;
+                    amax = fmaxf(amax, fabsf(x[b][i][j]));
+                }
+            }
+        amax = fold32(fold16(amax, MaxOp()), MaxOp());
+        const int e = row_exponent(amax);
+        mul[c] = attn_mul(a, e);
+#pragma unroll
+        for (int b = 0; b < NK; b++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float v = ldexpf(x[b][i / 4][i % 4], e);
+                const _Float16 p = (_Float16)v, rest = (_Float16)(v - (float)p);
+                qh[c][b][i] = STACK && col >= 8 ? rest : p;
+                ql[c][b][i] = rest;
+            }
+    }
+
+    floatx4 o[NC][ND];
+    float m[NC], l[NC];
+    int top[NC];  // Q8_0: biased exponent of the largest value scale
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+        m[c] = -INFINITY;
+        l[c] = 0.f;
+        top[c] = 0;
+#pragma unroll
+        for (int d = 0; d < ND; d++) o[c][d] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    Regs<D, Q8> x;
+    int64_t k0 = w.k0 + kChunk * wave;
+    Where at{}, next{};
+    if (k0 < w.k1) {
+        at = where<Q8>(a, w.s, w.h, k0, rec);
+        load_keys<D, Q8>(a, at, x);
+        load_values<D, Q8>(a, at, x);
+    }
+    for (; k0 < w.k1; k0 += kChunk * kWaves) {
+        const int64_t kn = k0 + kChunk * kWaves;
+        if (kn < w.k1) next = where<Q8>(a, w.s, w.h, kn, rec);
+        // scores: s[c][4 t + i] is token k0 + 8 g + 4 t + i of column c
+        float s[NC][8];
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            floatx4 sum[NC];
+#pragma unroll
+            for (int c = 0; c < NC; c++) sum[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int b = 0; b < NK; b++) {
+                half8 kf;
+                if constexpr (Q8) kf = codes8(x.k[t][b]);
+                else kf = __builtin_bit_cast(half8, x.k[t][b]);
+#pragma unroll
+                for (int c = 0; c < NC; c++) {
+                    floatx4 z = Q8 ? floatx4{0.f, 0.f, 0.f, 0.f} : sum[c];
+                    if constexpr (!STACK) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, ql[c][b], z, 0, 0, 0);
+                    z = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qh[c][b], z, 0, 0, 0);
+                    if constexpr (Q8) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++) sum[c][i] = fmaf(z[i], (float)x.ks[b][4 * t + i], sum[c][i]);
+                    } else {
+                        sum[c] = z;
+                    }
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; c++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    float v = sum[c][i];
+                    if constexpr (STACK)  // the other part's column: row_ror 8
+                        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
+                    s[c][4 * t + i] = attn_score(v, mul[c], a.softcap);
+                }
+        }
+        if (kn < w.k1) load_keys<D, Q8>(a, next, x);
+
+        const bool plain = k0 >= w.lo_all && k0 + kChunk <= w.hi_all && __ballot(!at.good) == 0;  // uniform
+        if (!plain) {
+#pragma unroll
+            for (int c = 0; c < NC; c++)
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int64_t k = k0 + 8 * g + j;
+                    if (!at.good || k < lo[c] || k >= hi[c]) s[c][j] = -INFINITY;
+                }
+        }
+        // what no row sees has no value, whatever the pool holds there.  What
+        // some rows see and others do not must not reach the others through 0 *
+        // infinity: such f16 values are taken out here and added by hand below
+        bool odd = false;
+        if (!plain) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int64_t k = k0 + 8 * g + j;
+                const bool any = at.good && k >= w.lo_any && k < w.hi_any, all = at.good && k >= w.lo_all && k < w.hi_all;
+                if constexpr (Q8) {
+#pragma unroll
+                    for (int b = 0; b < NK; b++) x.vs[b][j] = any ? x.vs[b][j] : (_Float16)0.f;
+                } else {
+                    const uint32_t sel = j & 1 ? 0xFFFF0000u : 0x0000FFFFu, exps = sel & 0x7C007C00u;
+#pragma unroll
+                    for (int d = 0; d < ND; d++) {
+                        const uint32_t v = x.v[d][j / 2];
+                        const bool inf = (v & exps) == exps;
+                        odd |= inf && any && !all;
+                        if (!any || (inf && !all)) x.v[d][j / 2] = v & ~sel;
+                    }
+                }
+            }
+        }
+        // 2^15: the f16 parts of a probability below 2^-14 keep their bits.  Q8_0: under the
+        // power of two that the finite value scales the row has seen stay below,
+        // |scale| < 2^(top - 14)
+        float grow[NC], unit[NC];
+        if constexpr (Q8) {
+            uint32_t es[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                es[j] = 0;
+#pragma unroll
+                for (int b = 0; b < NK; b++) {
+                    const _Float16 sc = x.vs[b][j];  // a bit cast of the element itself reads element 0
+                    const uint32_t u = __builtin_bit_cast(uint16_t, sc) & 0x7FFFu;
+                    es[j] = u > es[j] && u < 0x7C00u ? u : es[j];
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; c++) {
+                uint32_t e = 0;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int64_t k = k0 + 8 * g + j;
+                    const uint32_t u = plain || (k >= lo[c] && k < hi[c]) ? es[j] : 0u;
+                    e = u > e ? u : e;
+                }
+                const int now = (int)fold32(fold16((float)(e >> 10), MaxOp()), MaxOp());
+                const int up = now > top[c] ? now : top[c];
+                grow[c] = ldexpf(1.f, top[c] - up);
+                top[c] = up;
+                unit[c] = ldexpf(1.f, 29 - up);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < NC; c++) {
+                grow[c] = 1.f;
+                unit[c] = 32768.f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            float mx = s[c][0];
+#pragma unroll
+            for (int j = 1; j < 8; j++) mx = fmaxf(mx, s[c][j]);
+            mx = fmaxf(m[c], fold32(fold16(mx, MaxOp()), MaxOp()));
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            const float alpha = __builtin_amdgcn_exp2f(m[c] - ref);
+            m[c] = mx;
+            float ps = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                s[c][j] = __builtin_amdgcn_exp2f(s[c][j] - ref);
+                ps += s[c][j];
+            }
+            l[c] = fmaf(l[c], alpha, ps);
+            const float f = alpha * grow[c];
+            if (__ballot(f != 1.f)) {
+#pragma unroll
+                for (int d = 0; d < ND; d++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) o[c][d][i] *= f;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NK; b++) {
+            half8 v0, v1;
+            if constexpr (Q8) {
+                v0 = codes8(x.v[2 * b]);
+                v1 = codes8(x.v[2 * b + 1]);
+            } else {
+                v0 = __builtin_bit_cast(half8, x.v[2 * b]);
+                v1 = __builtin_bit_cast(half8, x.v[2 * b + 1]);
+            }
+#pragma unroll
+            for (int c = 0; c < NC; c++) {
+                half8 ph, pl;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    float p = s[c][j] * unit[c];
+                    if constexpr (Q8) p = s[c][j] == 0.f ? 0.f : p * (float)x.vs[b][j];
+                    const _Float16 hi_ = (_Float16)p, rest = (_Float16)(p - (float)hi_);
+                    ph[j] = STACK && col >= 8 ? rest : hi_;
+                    pl[j] = rest;
+                }
+                if constexpr (!STACK) {
+                    o[c][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl, o[c][2 * b], 0, 0, 0);
+                    o[c][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl, o[c][2 * b + 1], 0, 0, 0);
+                }
+                o[c][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, ph, o[c][2 * b], 0, 0, 0);
+                o[c][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, ph, o[c][2 * b + 1], 0, 0, 0);
+            }
+        }
+        if constexpr (!Q8) {
+            if (__ballot(odd)) {  // uniform; rare: an infinity or NaN that only some rows see
+                for (int j = 0; j < kChunk; j++) {
+                    const int64_t k = k0 + j;
+                    const int pg = kv_page(a.kv, w.s, k);
+                    if (pg < 0) continue;
+                    const int page = 1 << a.kv.page_shift;
+                    const _Float16 *v = reinterpret_cast<const _Float16 *>(a.kv.v + ((int64_t)pg * a.kv.heads + w.h) * rec) + ((int)k & (page - 1));
+#pragma unroll
+                    for (int d = 0; d < ND; d++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const float y = (float)v[(16 * d + 4 * g + i) * page];
+                            if (__builtin_isfinite(y) || (k >= w.lo_all && k < w.hi_all)) continue;
+#pragma unroll
+                            for (int c = 0; c < NC; c++)
+                                if (k >= lo[c] && k < hi[c]) o[c][d][i] += y;
+                        }
+                }
+            }
+        }
+        at = next;
+        if (kn < w.k1) load_values<D, Q8>(a, at, x);
+    }
+
+    // join the wavefronts
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+        l[c] = fold32(fold16(l[c], SumOp()), SumOp());
+        if (l[c] != l[c]) m[c] = INFINITY;  // a NaN score is no maximum, but its row is not one that saw nothing
+        if (g == 0) lstat[wave][16 * c + col] = make_float2(m[c], l[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+        const float down = Q8 ? ldexpf(1.f, top[c] - 29) : 1.f / 32768.f;
+        __syncthreads();
+        float M = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < kWaves; v++) M = fmaxf(M, lstat[v][16 * c + col].x);
+        const float f = m[c] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[c] - M) * down;
+#pragma unroll
+        for (int d = 0; d < ND; d++) {
+            floatx4 y = o[c][d];
+#pragma unroll
+            for (int i = 0; i < 4; i++) y[i] = f == 0.f ? 0.f : y[i] * f;
+            *reinterpret_cast<floatx4 *>(&lo_[wave][col][16 * d + 4 * g]) = y;
+        }
+        __syncthreads();
+        const int rows = w.nrows - 16 * c < (STACK ? 8 : 16) ? w.nrows - 16 * c : (STACK ? 8 : 16);
+        for (int e = (int)threadIdx.x; e < rows * (D / 4); e += 64 * kWaves) {
+            const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
+            floatx4 y{};
+            float Mr = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int v = 0; v < kWaves; v++) Mr = fmaxf(Mr, lstat[v][16 * c + r].x);
+#pragma unroll
+            for (int v = 0; v < kWaves; v++) {
+                const float2 st = lstat[v][16 * c + r];
+                if (st.x != -INFINITY) L = fmaf(st.y, __builtin_amdgcn_exp2f(st.x - Mr), L);
+                floatx4 z = *reinterpret_cast<const floatx4 *>(&lo_[v][r][d]);
+                if constexpr (STACK) z += *reinterpret_cast<const floatx4 *>(&lo_[v][r + 8][d]);
+                y += z;
+            }
+            const int row = w.r0 + 16 * c + r, t = row / a.G, hq = w.h * a.G + (row - t * a.G);
+            const int64_t rh = (int64_t)(w.nw.first + t) * a.Hq + hq;
+            if (a.splits == 1) {
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                for (int i = 0; i < 4; i++) y[i] *= inv;
+                *reinterpret_cast<floatx4 *>(a.out + rh * D + d) = y;
+            } else {
+                const int64_t at_ = rh * a.splits + w.split;
+                if (Mr != -INFINITY) *reinterpret_cast<floatx4 *>(a.part + at_ * D + d) = y;
+                if (d == 0) a.stat[at_] = make_float2(Mr, L);
+            }
+        }
+    }
+}
+
+// Rows that several workgroups share: out = sum_s 2^(m_s - M) part_s / sum_s
+// 2^(m_s - M) l_s.  W wavefronts a row take every W-th split.
+template <int D, int W>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+    constexpr int NV = (D + 63) / 64;
+    __shared__ float acc[4][D];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int64_t rh = (a.block0 + blockIdx.x) * (4 / W) + (W == 4 ? 0 : wave);
+    if (rh >= (int64_t)a.kv.rows * a.Hq) return;  // W 1: whole wavefronts, no barrier follows
+    const int n = (int)(rh / a.Hq);
+    const int s = kv_row_seq(a.kv, n);
+    if (s < 0) return;
+    const KvNew nw = kv_new(a.kv, s);
+    if (n - nw.first >= nw.count) return;
+    const float2 *st = a.stat + rh * a.splits;
+    const float *part = a.part + rh * a.splits * D;
+    float M = -INFINITY;
+    for (int i = lane; i < a.splits; i += 64) M = fmaxf(M, st[i].x);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+    float y[NV] = {}, L = 0.f;
+    for (int i = lane; i < a.splits; i += 64)
+        if (st[i].x != -INFINITY) L = fmaf(st[i].y, __builtin_amdgcn_exp2f(st[i].x - M), L);
+    L = wave_sum(L);
+    const int w0 = W == 4 ? wave : 0;
+#pragma unroll 4
+    for (int i = w0; i < a.splits; i += W) {
+        const float mi = st[i].x;
+        if (mi == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f(mi - M);
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+            if (64 * v + lane < D) y[v] = fmaf(part[(int64_t)i * D + 64 * v + lane], f, y[v]);
+    }
+    if constexpr (W == 4) {
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+            if (64 * v + lane < D) acc[wave][64 * v + lane] = y[v];
+        __syncthreads();
+        if (wave != 0) return;
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+            if (64 * v + lane < D) y[v] = (acc[0][64 * v + lane] + acc[1][64 * v + lane]) + (acc[2][64 * v + lane] + acc[3][64 * v + lane]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int v = 0; v < NV; v++)
+        if (64 * v + lane < D) a.out[rh * D + 64 * v + lane] = y[v] * inv;
+}
+
+// How a call is shared out: rows of a tile, row tiles of a sequence and head, splits of the tokens.
+struct Plan {
+    int mode;  // 0, 1, 2: attn_few_kernel
+    int tiles, splits;
+    int64_t blocks;
+};
+
+Plan plan_of(const qmm_kv_cache &c, const qmm_kv_batch &b, int64_t q_heads) {
+    const int64_t G = q_heads / c.heads, rows = b.max_new * G, units = b.seqs * c.heads;
+    Plan p;
+    p.mode = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
+    const int64_t rt = p.mode == 0 ? 8 : 16 * p.mode;
+    p.tiles = (int)((rows + rt - 1) / rt);
+    const int64_t chunks = (b.max_pages * c.page + kChunk - 1) / kChunk;
+    const int64_t want = (512 + units * p.tiles - 1) / (units * p.tiles), most = (chunks + 2 * kLeast - 1) / (2 * kLeast);
+    const int64_t s = want < most ? want : most;
+    p.splits = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+    p.blocks = units * p.tiles * p.splits;
+    return p;
+}
+
+constexpr int64_t kBlocks = int64_t(1) << 23;  // of a launch: fewer than 2^32 threads
+
+template <int D, bool Q8>
+hipError_t launch_few(AttnArgs a, const Plan &p, hipStream_t st) {
+    for (int64_t b = 0; b < p.blocks; b += kBlocks) {
+        a.block0 = b;
+        const dim3 grid((unsigned)(p.blocks - b < kBlocks ? p.blocks - b : kBlocks)), block(64 * kWaves);
+        if (p.mode == 0) hipLaunchKernelGGL((attn_few_kernel<D, Q8, 0>), grid, block, 0, st, a);
+        else if (p.mode == 1) hipLaunchKernelGGL((attn_few_kernel<D, Q8, 1>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attn_few_kernel<D, Q8, 2>), grid, block, 0, st, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <int D>
+hipError_t launch_d(AttnArgs a, int dtype, const Plan &p, hipStream_t st) {
+    const hipError_t e = dtype == QMM_Q8_0 ? launch_few<D, true>(a, p, st) : launch_few<D, false>(a, p, st);
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int64_t rh = (int64_t)a.kv.rows * a.Hq;
+    const bool wide = p.splits > 8;
+    const int64_t blocks = wide ? rh : (rh + 3) / 4;
+    for (int64_t b = 0; b < blocks; b += kBlocks) {
+        a.block0 = b;
+        const dim3 grid((unsigned)(blocks - b < kBlocks ? blocks - b : kBlocks));
+        if (wide) hipLaunchKernelGGL((attn_join_kernel<D, 4>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((attn_join_kernel<D, 1>), grid, dim3(256), 0, st, a);
+        const hipError_t e2 = hipGetLastError();
+        if (e2 != hipSuccess) return e2;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+int64_t attention_work_bytes(const qmm_kv_cache &cache, const qmm_kv_batch &batch, int64_t q_heads) {
+    const Plan p = plan_of(cache, batch, q_heads);
+    return p.splits == 1 ? 0 : batch.rows * q_heads * p.splits * (4 * (int64_t)cache.dim + 8);
+}
+
+hipError_t launch_attention(const qmm_kv_cache &cache, const qmm_kv_batch &batch, const float *Q, int64_t q_stride,
+                            int64_t q_heads, double scale, bool causal, int64_t window, double softcap, float *out,
+                            void *work, hipStream_t st) {
+    const Plan p = plan_of(cache, batch, q_heads);
+    AttnArgs a{};
+    a.Q = Q;
+    a.out = out;
+    a.part = (float *)work;
+    a.stat = (float2 *)((char *)work + batch.rows * q_heads * p.splits * 4 * (int64_t)cache.dim);
+    a.q_stride = q_stride;
+    a.window = window;
+    a.scale = (float)scale;
+    a.softcap = (float)softcap;
+    a.Hq = (int)q_heads;
+    a.G = (int)(q_heads / cache.heads);
+    a.splits = p.splits;
+    a.tiles = p.tiles;
+    a.causal = causal;
+    a.kv = kv_args(cache, batch);
+    switch (cache.dim) {
+    case 64: return launch_d<64>(a, cache.dtype, p, st);
+    case 96: return launch_d<96>(a, cache.dtype, p, st);
+    case 128: return launch_d<128>(a, cache.dtype, p, st);
+    case 192: return launch_d<192>(a, cache.dtype, p, st);
+    case 256: return launch_d<256>(a, cache.dtype, p, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qmm

@@ -122,6 +122,13 @@ hipError_t launch_kv_append(const qmm_kv_cache &cache, const qmm_kv_batch &batch
                             const int32_t *pos, const float *k_norm, const float *q_norm, double eps, const float *Q,
                             int64_t q_stride, int64_t q_heads, float *q_out, hipStream_t st);
 
+// Attention over the paged cache (qmm_attn.hip).  `work` holds the work bytes
+// of the same sizes (NULL where they are 0).
+int64_t attention_work_bytes(const qmm_kv_cache &cache, const qmm_kv_batch &batch, int64_t q_heads);
+hipError_t launch_attention(const qmm_kv_cache &cache, const qmm_kv_batch &batch, const float *Q, int64_t q_stride,
+                            int64_t q_heads, double scale, bool causal, int64_t window, double softcap, float *out,
+                            void *work, hipStream_t st);
+
 // The norms after and before a block with its gate and residual scale
 // (qmm_norm.hip): K <= 2^28, block / w_post / gate / residual_out / w_pre / H /
 // (scales, quants) may be NULL as qmm_block_norm allows.

@@ -570,6 +570,43 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
                   const float *k_norm, const float *q_norm, double eps, const float *Q, int64_t q_stride, int64_t q_heads,
                   float *q_out, void *stream);
 
+/* Attention of the new tokens over the cache (their own keys and values are in
+ * it already): one decoded token, drafted tokens, a prompt or a chunk of one, or
+ * (causal 0) queries over another sequence's states.  Query head h looks at
+ * key-value head h / (q_heads / heads):
+ *     x_j = scale * Q[n][h] . key_j        (softcap c > 0: c tanh(x_j / c))
+ *     out[n][h] = sum_j p_j value_j,  p = softmax of x over the visible tokens j
+ * j is visible to the token with index i if it has a page, j < lens[s], and, with
+ * causal, j <= i, and, with a window w > 0, j > i - w.  A row that sees nothing
+ * gets zeros, whatever the cache holds; what a row does not see does not reach
+ * it, infinities and NaN neither.
+ * Queries and probabilities are split in two f16 parts under a power of two and
+ * multiplied on the matrix cores, f32 accumulation, statistics in f32: f32 class.
+ * With S_j = |scale| sum_d |q_d key_jd|, the error of a score is at most
+ *     e_j = 2^-17 S_j + 2^-36 |scale| max_d |q_d| sum_d |key_jd| + 2^-21 softcap
+ * and with e its largest value over the n visible tokens,
+ *     |out - exact| <= (2 e + 2^-17 + n 2^-26) sum_j p_j (|value_j| + |exact|) + n 2^-32 max_j |value_j|
+ * (the last over all dims of the visible tokens).  These count every rounding at its worst;
+ * random data come within 1e-6 or so of the output's size.
+ *   Q       device f32, row n's q_heads heads of dim values at Q + n * q_stride
+ *           (0: q_heads * dim; a multiple of 4), 16-B aligned
+ *   q_heads a multiple of cache->heads, at most 2^16, else QMM_ERR_SHAPE
+ *   scale   finite; softcap finite, >= 0; window >= 0, and 0 unless causal: else
+ *           QMM_ERR_VALUE
+ *   out     device f32 [rows][q_heads * dim], 16-B aligned; rows of sequences
+ *           overwritten, padding left as it is; overlaps nothing
+ *   work    device scratch of at least qmm_attention_work_bytes(...) bytes
+ *           (work_bytes; less is QMM_ERR_SCRATCH), 16-B aligned; NULL where that
+ *           is 0.  Needs no initial value; clobbered.  Calls that overlap in time
+ *           (two streams, two captured graphs) need separate work.
+ * A row's result does not depend on the other sequences of the call, as long as
+ * the sizes of cache, batch and q_heads are the same (they choose the form and
+ * how the tokens are shared out).  Results are bitwise reproducible. */
+int64_t qmm_attention_work_bytes(const qmm_kv_cache *cache, const qmm_kv_batch *batch, int64_t q_heads);
+int qmm_attention(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const float *Q, int64_t q_stride, int64_t q_heads,
+                  double scale, int causal, int64_t window, double softcap, float *out, void *work, int64_t work_bytes,
+                  void *stream);
+
 /* Which arithmetic qmm_gemm uses for these sizes: 0 = f32 (GEMV family),
  * 1 = f16 matrix-core GEMM, or a negative status for invalid arguments. */
 int qmm_gemm_path(int dtype, int64_t M, int64_t K, int64_t N);

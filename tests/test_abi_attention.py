@@ -96,6 +96,41 @@ def test_kv_append_rejects(kw, code):
     assert append(**kw) == code
 
 
+def attention(Q=A, q_stride=0, q_heads=8, scale=0.1, causal=1, window=0, softcap=0.0, out=A, work=A, work_bytes=BIG,
+              no_cache=False, no_batch=False, **kw):
+    c, b, rest = structs(kw)
+    assert not rest
+    return q.lib().qmm_attention(None if no_cache else ctypes.addressof(c), None if no_batch else ctypes.addressof(b), Q,
+                                 q_stride, q_heads, scale, causal, window, softcap, out, work, work_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", SIZES + [
+    (dict(q_heads=0), q.QMM_ERR_SHAPE), (dict(q_heads=2), q.QMM_ERR_SHAPE), (dict(q_heads=10), q.QMM_ERR_SHAPE),
+    (dict(q_heads=65540), q.QMM_ERR_SHAPE), (dict(q_stride=1020), q.QMM_ERR_SHAPE), (dict(q_stride=1026), q.QMM_ERR_SHAPE),
+    (dict(heads=1, q_heads=64, seqs=1, max_new=1 << 26, rows=1 << 26), q.QMM_ERR_SHAPE),
+    (dict(scale=math.nan), q.QMM_ERR_VALUE), (dict(scale=1e300), q.QMM_ERR_VALUE), (dict(softcap=-1.0), q.QMM_ERR_VALUE),
+    (dict(softcap=math.inf), q.QMM_ERR_VALUE), (dict(window=-1), q.QMM_ERR_VALUE),
+    (dict(window=5, causal=0), q.QMM_ERR_VALUE), (dict(Q=0), q.QMM_ERR_NULL), (dict(out=0), q.QMM_ERR_NULL),
+    (dict(Q=A + 4), q.QMM_ERR_ALIGN), (dict(out=A + 8), q.QMM_ERR_ALIGN),
+])
+def test_attention_rejects(kw, code):
+    assert attention(**kw) == code
+
+
+def test_attention_work_is_checked():
+    kw = dict(max_pages=1000, pages=4000)
+    c, b, _ = structs(kw)
+    n = q.lib().qmm_attention_work_bytes(ctypes.addressof(c), ctypes.addressof(b), 8)
+    assert n > 0
+    assert attention(work=0, work_bytes=0, **kw) == q.QMM_ERR_NULL
+    assert attention(work=A + 8, work_bytes=n, **kw) == q.QMM_ERR_ALIGN
+    assert attention(work=A, work_bytes=n - 1, **kw) == q.QMM_ERR_SCRATCH
+    for bad in (dict(dtype=3), dict(seqs=0), dict(dim=80)):
+        c, b, _ = structs(bad)
+        assert q.lib().qmm_attention_work_bytes(ctypes.addressof(c), ctypes.addressof(b), 8) == 0
+    assert q.lib().qmm_attention_work_bytes(None, ctypes.addressof(b), 8) == 0
+
+
 def test_pool_bytes():
     assert q.kv_pool_bytes(1, 10, 64, 8, 128) == 10 * 64 * 8 * 128 * 2
     assert q.kv_pool_bytes(8, 10, 64, 8, 128) == 10 * 64 * 8 * (128 + 8)
@@ -109,4 +144,5 @@ def test_valid_calls_without_gpu_report_device():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present; covered by the GPU tests")
     assert rope() == q.QMM_ERR_DEVICE and freqs() == q.QMM_ERR_DEVICE and append() == q.QMM_ERR_DEVICE
+    assert attention() == q.QMM_ERR_DEVICE and attention(causal=0, starts=A, rows=1, dtype=8) == q.QMM_ERR_DEVICE
     assert append(Q=0, q_out=0, q_heads=0, freqs=0, rot=0, layout=9, dtype=8, starts=A, rows=1) == q.QMM_ERR_DEVICE
