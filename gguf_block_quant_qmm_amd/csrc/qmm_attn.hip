@@ -359,7 +359,10 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
                     for (int d = 0; d < ND; d++)
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            const float y = (float)v[(16 * d + 4 * g + i) * page];
+                            // addresses made here each time, not kept in registers through the main loop
+                            int dim = 16 * d + 4 * g + i;
+                            asm volatile("" : "+v"(dim));
+                            const float y = (float)v[dim * page];
                             if (__builtin_isfinite(y) || (k >= w.lo_all && k < w.hi_all)) continue;
 #pragma unroll
                             for (int c = 0; c < NC; c++)
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
 
 // How a call is shared out: rows of a tile, row tiles of a sequence and head, splits of the tokens.
 struct Plan {
-    int mode;  // 0, 1, 2: attn_few_kernel
+    int mode;  // 0, 1, 2: attn_few_kernel; 3: the form for many rows
     int tiles, splits;
     int64_t blocks;
 };
@@ -486,11 +489,11 @@ struct Plan {
 Plan plan_of(const qmm_kv_cache &c, const qmm_kv_batch &b, int64_t q_heads) {
     const int64_t G = q_heads / c.heads, rows = b.max_new * G, units = b.seqs * c.heads;
     Plan p;
-    p.mode = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
-    const int64_t rt = p.mode == 0 ? 8 : 16 * p.mode;
+    p.mode = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
+    const int64_t rt = p.mode == 0 ? 8 : p.mode == 3 ? kPromptRows : 16 * p.mode;
     p.tiles = (int)((rows + rt - 1) / rt);
-    const int64_t chunks = (b.max_pages * c.page + kChunk - 1) / kChunk;
-    const int64_t want = (512 + units * p.tiles - 1) / (units * p.tiles), most = (chunks + 2 * kLeast - 1) / (2 * kLeast);
+    const int64_t least = p.mode == 3 ? 4 * kPromptChunk : 2 * kLeast * kChunk;  // tokens of a split
+    const int64_t want = (512 + units * p.tiles - 1) / (units * p.tiles), most = (b.max_pages * c.page + least - 1) / least;
     const int64_t s = want < most ? want : most;
     p.splits = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
     p.blocks = units * p.tiles * p.splits;
@@ -515,7 +518,9 @@ hipError_t launch_few(AttnArgs a, const Plan &p, hipStream_t st) {
 
 template <int D>
 hipError_t launch_d(AttnArgs a, int dtype, const Plan &p, hipStream_t st) {
-    const hipError_t e = dtype == QMM_Q8_0 ? launch_few<D, true>(a, p, st) : launch_few<D, false>(a, p, st);
+    const hipError_t e = p.mode == 3           ? launch_attn_prompt(a, dtype, D, p.blocks, st)
+                         : dtype == QMM_Q8_0 ? launch_few<D, true>(a, p, st)
+                                             : launch_few<D, false>(a, p, st);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t rh = (int64_t)a.kv.rows * a.Hq;
     const bool wide = p.splits > 8;

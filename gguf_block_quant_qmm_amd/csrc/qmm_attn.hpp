@@ -133,4 +133,8 @@ __device__ __forceinline__ half8 codes8(u32x2_t v) {
     return half8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
+// The form for many rows (qmm_attn_prompt.hip): rows of a workgroup, tokens of a tile.
+constexpr int kPromptRows = 128, kPromptChunk = 64;
+hipError_t launch_attn_prompt(const AttnArgs &a, int dtype, int D, int64_t blocks, hipStream_t st);
+
 }  // namespace qmm

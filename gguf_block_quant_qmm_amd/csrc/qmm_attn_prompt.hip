@@ -1,0 +1,413 @@
+// qmm_attn_prompt.hip -- attention of many new tokens over the paged cache (a
+// prompt, a chunk of one, long drafts; include/qmm.h, qmm_attention).
+//
+// A workgroup takes 128 rows (new tokens x the G query heads of one key-value
+// head, so that they share every key) and 64 tokens of the cache at a time; a
+// wavefront has 32 rows as the columns of v_mfma_f32_32x32x16_f16:
+//   scores^T = K Q^T   A = 32 tokens' keys, B = the queries (registers)
+//   out^T   += V^T P^T A = 32 dims of the values, B = the probabilities, which
+//                      stay in the lane that made them: row r of the first
+//                      product is token r with bits 2 and 3 exchanged, so a lane's
+//                      16 scores are two runs of 8 neighbouring tokens
+// f32 class: queries and probabilities in two f16 parts, two steps for one.
+// Q8_0: codes times (both parts of) the queries, one block's product scaled by
+// the token's key scale in f32; values as hi + lo, both f16 and exact together
+// (a code times a scale has 18 bits), three steps for one.
+//
+// Bound by the matrix cores: 4 D products a score take 2048 cycles of a SIMD per
+// wavefront and tile at D = 128, its softmax about 1100 of the vector ALU; two
+// wavefronts a SIMD let one's softmax run under the other's products.  Keys and
+// values go through registers to LDS (rows padded by 16 bytes: eight neighbouring rows
+// then start in eight different groups of four banks), the next tile's loads under
+// way during the products.
+//
+// The running reference of the exponentials moves only when a row's maximum
+// passes it by 2^8: probabilities are up to 2^15 instead of 1, which both f16
+// parts hold, and the outputs are rescaled once or twice a row instead of every tile.
+#include "qmm_attn.hpp"
+
+namespace qmm {
+
+namespace {
+
+constexpr int CH = kPromptChunk, RT = kPromptRows;
+
+// One tile on its way from memory to LDS.  Wavefront w brings the keys of the
+// tile's w-th run of 16 tokens (neighbours in their page: one piece of memory, from a
+// uniform address) and D/4 dims of all 64 tokens' values.
+template <int D, bool Q8> struct Stage;
+template <int D> struct Stage<D, false> {
+    u32x4_t k[D / 32], v[D / 32];
+};
+template <int D> struct Stage<D, true> {
+    // the wavefront's 8 dims of step i lie in one block: block (w D/4 + 8 i) / 32
+    static constexpr int NB = D == 64 || D == 128 ? 1 : D == 256 ? 2 : D / 32;
+    static __device__ constexpr int at(int i) { return NB == 1 ? 0 : NB == 2 ? i / 4 : i; }
+    u32x2_t k[D / 32], v[D / 32];
+    half8 vs[NB];
+    u32x2_t ks;  // the thread's 4 tokens' scales of one block
+};
+
+template <int D, bool Q8> struct Tile {  // in LDS
+    static constexpr int KP = D + 8, VP = CH + 8;
+    _Float16 k[CH][KP];
+    _Float16 v[Q8 ? 2 : 1][D][VP];
+    _Float16 ks[Q8 ? D / 32 : 1][CH];
+    int odd;
+};
+
+// Token t of a tile <-> row of the first product: bits 2 and 3 exchanged.
+__device__ __forceinline__ int swap23(int t) { return (t & ~12) | ((t & 4) << 1) | ((t & 8) >> 1); }
+
+// A token's distance from the tile's first, cut to what the tile can tell apart.
+__device__ __forceinline__ int within(int64_t x) { return (int)(x < 0 ? 0 : x > CH ? CH : x); }
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(const AttnArgs a) {
+    constexpr int NS = D / 32, NK = D / 16, ND = D / 32;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    Tile<D, Q8> &T = *reinterpret_cast<Tile<D, Q8> *>(lds);
+    AttnShare w;
+    if (!attn_share<RT, CH>(a, 2, w)) return;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, hh = lane >> 5;
+    const int page = 1 << a.kv.page_shift;
+    const int64_t rec = kv_record(Q8 ? QMM_Q8_0 : QMM_F16, page, D);
+    const int r = 32 * wave + col;
+    const bool on = r < w.nrows, wave_on = 32 * wave < w.nrows;
+    const int row = w.r0 + (on ? r : 0), t = row / a.G, hq = w.h * a.G + (row - t * a.G);
+    int64_t lo, hi;
+    attn_sees(a, w.nw, t, lo, hi);
+    if (!on) lo = hi = 0;
+
+    half8 qh[NK], ql[NK];
+    float mul;
+    {
+        const float *q = a.Q + (int64_t)(w.nw.first + t) * a.q_stride + (int64_t)hq * D + 8 * hh;
+        float amax = 0.f;
+        floatx4 x[NK][2];
+#pragma unroll
+        for (int b = 0; b < NK; b++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                x[b][i] = *reinterpret_cast<const floatx4 *>(q + 16 * b + 4 * i);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    if (!on) x[b][i][j] = 0.f;
+                    amax = fmaxf(amax, fabsf(x[b][i][j]));
+                }
+            }
+        amax = fold32(amax, MaxOp());
+        const int e = row_exponent(amax);
+        mul = attn_mul(a, e);
+        // a negative scale goes into the queries, so that the largest product is the largest score
+        const bool neg = mul < 0.f;
+        mul = fmaxf(fabsf(mul), 0x1p-126f);  // above 0: a masked -inf stays one
+#pragma unroll
+        for (int b = 0; b < NK; b++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float s = x[b][i / 4][i % 4], v = ldexpf(neg ? -s : s, e);
+                const _Float16 p = (_Float16)v;
+                qh[b][i] = p;
+                ql[b][i] = (_Float16)(v - (float)p);
+            }
+    }
+    floatx16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[d][i] = 0.f;
+    float base = -INFINITY, l = 0.f;
+
+    Stage<D, Q8> st;
+    int good = 0;  // which of the tile's four runs of 16 tokens have a page
+    const int g = lane & 7, d0 = wave * (D / 4) + (lane >> 3);  // the values' tokens 8g .. 8g+7 and dims d0 + 8i
+    auto load = [&](int64_t k0) {
+        int pg[4];
+        good = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            pg[i] = __builtin_amdgcn_readfirstlane(kv_page(a.kv, w.s, k0 + 16 * i));
+            good |= (pg[i] >= 0) << i;
+            pg[i] = pg[i] < 0 ? 0 : pg[i];  // masked
+        }
+        auto record = [&](int run) {
+            const int p01 = run & 1 ? pg[1] : pg[0], p23 = run & 1 ? pg[3] : pg[2];
+            return ((int64_t)(run & 2 ? p23 : p01) * a.kv.heads + w.h) * rec;
+        };
+        const uint8_t *kr = a.kv.k + record(wave);
+        const int kslot = (int)(k0 + 16 * wave) & (page - 1);
+#pragma unroll
+        for (int i = 0; i < NS; i++) {
+            if constexpr (Q8) st.k[i] = *reinterpret_cast<const u32x2_t *>(kr + kslot * D + 8 * lane + 512 * i);
+            else st.k[i] = *reinterpret_cast<const u32x4_t *>(kr + 2 * kslot * D + 16 * lane + 1024 * i);
+        }
+        if constexpr (Q8) {
+            if (tid < 16 * NS) {
+                const int b = tid >> 4, key = 4 * (tid & 15);
+                const uint8_t *p = a.kv.k + record(key >> 4) + page * D;
+                st.ks = *reinterpret_cast<const u32x2_t *>(p + 2 * (b * page + ((int)(k0 + key) & (page - 1))));
+            }
+        }
+        const uint8_t *vr = a.kv.v + record(g >> 1);
+        const int vslot = (int)(k0 + 8 * g) & (page - 1);
+#pragma unroll
+        for (int i = 0; i < NS; i++) {
+            const int at = (d0 + 8 * i) * page + vslot;
+            if constexpr (Q8) st.v[i] = *reinterpret_cast<const u32x2_t *>(vr + at);
+            else st.v[i] = *reinterpret_cast<const u32x4_t *>(vr + 2 * at);
+        }
+        if constexpr (Q8) {
+#pragma unroll
+            for (int i = 0; i < NS; i++)
+                if (i == 0 || st.at(i) != st.at(i - 1))
+                    st.vs[st.at(i)] = *reinterpret_cast<const half8 *>(
+                        vr + page * D + 2 * (((wave * (D / 4) + 8 * i) >> 5) * page + vslot));
+        }
+    };
+    // the tile to LDS; `plain`: every row sees all of it.  What no row sees has no
+    // value, whatever the pool holds; infinities and NaN that only some rows see are
+    // taken out (T.odd) and added by hand
+    auto store = [&](int64_t k0, bool plain) {
+#pragma unroll
+        for (int i = 0; i < NS; i++) {
+            const int e = lane + 64 * i, key = e / (D / 8), c = e - key * (D / 8);
+            half8 x;
+            if constexpr (Q8) x = codes8(st.k[i]);
+            else x = __builtin_bit_cast(half8, st.k[i]);
+            *reinterpret_cast<half8 *>(&T.k[16 * wave + swap23(key)][8 * c]) = x;
+        }
+        if constexpr (Q8) {
+            if (tid < 16 * NS) *reinterpret_cast<u32x2_t *>(&T.ks[tid >> 4][4 * (tid & 15)]) = st.ks;
+        }
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < NS; i++) {
+            const int d = d0 + 8 * i;
+            half8 x, y;
+            if constexpr (Q8) {
+                // v = 2^7 x + y exactly: 2^7 x is v to 11 bits or to 2^-17, y the rest
+                const half8 cd = codes8(st.v[i]);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float v = (float)cd[j] * (float)st.vs[st.at(i)][j];
+                    x[j] = (_Float16)(v * 0.0078125f);
+                    y[j] = (_Float16)fmaf((float)x[j], -128.f, v);
+                }
+            } else {
+                x = __builtin_bit_cast(half8, st.v[i]);
+            }
+            if (!plain) {
+                const bool has = good >> (g >> 1) & 1;
+                const int any0 = within(w.lo_any - k0) - 8 * g, any1 = within(w.hi_any - k0) - 8 * g;
+                const int all0 = within(w.lo_all - k0) - 8 * g, all1 = within(w.hi_all - k0) - 8 * g;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const bool any = has && j >= any0 && j < any1, all = has && j >= all0 && j < all1;
+                    const bool inf = !__builtin_isfinite((float)x[j]);
+                    odd |= inf && any && !all;
+                    if (!any || (inf && !all)) {
+                        x[j] = (_Float16)0.f;
+                        if constexpr (Q8) y[j] = (_Float16)0.f;
+                    }
+                }
+            }
+            *reinterpret_cast<half8 *>(&T.v[0][d][8 * g]) = x;
+            if constexpr (Q8) *reinterpret_cast<half8 *>(&T.v[1][d][8 * g]) = y;
+        }
+        if (odd) T.odd = 1;
+    };
+
+    if (w.k0 < w.k1) load(w.k0);
+    for (int64_t k0 = w.k0; k0 < w.k1; k0 += CH) {
+        const bool plain = k0 >= w.lo_all && k0 + CH <= w.hi_all && good == 15;  // uniform
+        const int seen = good;
+        if (tid == 0) T.odd = 0;
+        __syncthreads();  // the last tile's reads are done
+        store(k0, plain);
+        __syncthreads();
+        if (k0 + CH < w.k1) load(k0 + CH);
+        if (!wave_on) continue;
+        floatx16 s[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) s[u][i] = 0.f;
+            if constexpr (Q8) {
+#pragma unroll
+                for (int b = 0; b < D / 32; b++) {
+                    floatx16 z;
+#pragma unroll
+                    for (int i = 0; i < 16; i++) z[i] = 0.f;
+#pragma unroll
+                    for (int f = 0; f < 2; f++) {
+                        const half8 kf = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][32 * b + 16 * f + 8 * hh]);
+                        z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[2 * b + f], z, 0, 0, 0);
+                        z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[2 * b + f], z, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int f = 0; f < 2; f++) {
+                        const half8 sc = *reinterpret_cast<const half8 *>(&T.ks[b][32 * u + 16 * f + 8 * hh]);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) s[u][8 * f + i] = fmaf(z[8 * f + i], (float)sc[i], s[u][8 * f + i]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < NK; b++) {
+                    const half8 kf = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][16 * b + 8 * hh]);
+                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[b], s[u], 0, 0, 0);
+                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[b], s[u], 0, 0, 0);
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float mm = mul;
+        if (a.softcap > 0.f) {  // uniform
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) s[u][i] = attn_score(s[u][i], mul, a.softcap);
+            mm = 1.f;
+        }
+        if (!plain) {
+            // register i of half hh is token 16 (i / 8) + 8 hh + i % 8 of its 32
+            const int from = within(lo - k0) - 8 * hh, end = within(hi - k0) - 8 * hh;
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int j = 32 * u + 16 * (i >> 3) + (i & 7);
+                    if (!(seen >> (2 * u + (i >> 3)) & 1) || j < from || j >= end) s[u][i] = -INFINITY;
+                }
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) mx = fmaxf(mx, s[u][i]);
+        mx = fold32(mx, MaxOp()) * mm;
+        if (__ballot(mx > base + 15.f)) {
+            const float to = mx > base ? mx - 7.f : base;
+            const float alpha = base == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - to);
+            base = to;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < ND; d++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) o[d][i] *= alpha;
+        }
+        const float sub = base == -INFINITY ? 0.f : -base;
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], mm, sub));
+                l += s[u][i];
+            }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < 4; f++) {
+            half8 ph, pl;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float p = s[f >> 1][8 * (f & 1) + i];
+                ph[i] = (_Float16)p;
+                pl[i] = (_Float16)fmaf((float)ph[i], -1.f, p);
+            }
+            half8 pd;
+            if constexpr (Q8) pd = ph * (_Float16)0.0078125f;
+#pragma unroll
+            for (int d = 0; d < ND; d++) {
+                const half8 vf = *reinterpret_cast<const half8 *>(&T.v[0][32 * d + col][16 * f + 8 * hh]);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pl, o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, ph, o[d], 0, 0, 0);
+                if constexpr (Q8) {
+                    const half8 vl = *reinterpret_cast<const half8 *>(&T.v[1][32 * d + col][16 * f + 8 * hh]);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl, pd, o[d], 0, 0, 0);
+                }
+            }
+        }
+        if (!plain && T.odd) {  // rare: infinities or NaN that only some rows see
+            for (int j = 0; j < CH; j++) {
+                const int64_t k = k0 + j;
+                if (k >= w.lo_all && k < w.hi_all) continue;
+                const int pg = kv_page(a.kv, w.s, k);
+                if (pg < 0) continue;
+                const uint8_t *p = a.kv.v + ((int64_t)pg * a.kv.heads + w.h) * rec;
+                const int slot = (int)k & (page - 1);
+#pragma unroll
+                for (int d = 0; d < ND; d++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        // addresses made here each time, not kept in registers through the main loop
+                        int dim = 32 * d + 8 * (i >> 2) + 4 * hh + (i & 3);
+                        asm volatile("" : "+v"(dim));
+                        float y;
+                        if constexpr (Q8)
+                            y = (float)reinterpret_cast<const int8_t *>(p)[dim * page + slot] *
+                                (float)reinterpret_cast<const _Float16 *>(p + page * D)[(dim >> 5) * page + slot];
+                        else
+                            y = (float)reinterpret_cast<const _Float16 *>(p)[dim * page + slot];
+                        if (!__builtin_isfinite(y) && k >= lo && k < hi) o[d][i] += y;
+                        __builtin_amdgcn_sched_barrier(0);  // one at a time: no registers for a rare case
+                    }
+            }
+        }
+    }
+    if (!wave_on) return;
+    l = fold32(l, SumOp());
+    if (l != l) base = INFINITY;  // a NaN score is no maximum, but its row is not one that saw nothing
+    if (!on) return;
+    const int64_t rh = (int64_t)(w.nw.first + t) * a.Hq + hq;
+    const bool none = base == -INFINITY;
+    float f = Q8 ? 128.f : 1.f;
+    float *to = a.out + rh * D;
+    if (a.splits > 1) {
+        const int64_t at = rh * a.splits + w.split;
+        if (hh == 0) a.stat[at] = make_float2(base, l);
+        if (none) return;
+        to = a.part + at * D;
+    } else {
+        f = none ? 0.f : f / l;
+    }
+#pragma unroll
+    for (int d = 0; d < ND; d++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            floatx4 y;
+#pragma unroll
+            for (int j = 0; j < 4; j++) y[j] = o[d][4 * i + j] * f;
+            *reinterpret_cast<floatx4 *>(to + 32 * d + 8 * i + 4 * hh) = y;
+        }
+}
+
+template <int D>
+hipError_t launch_d(AttnArgs a, int dtype, int64_t blocks, hipStream_t st) {
+    constexpr int64_t kBlocks = int64_t(1) << 23;
+    for (int64_t b = 0; b < blocks; b += kBlocks) {
+        a.block0 = b;
+        const dim3 grid((unsigned)(blocks - b < kBlocks ? blocks - b : kBlocks));
+        if (dtype == QMM_Q8_0) hipLaunchKernelGGL((attn_prompt_kernel<D, true>), grid, dim3(256), sizeof(Tile<D, true>), st, a);
+        else hipLaunchKernelGGL((attn_prompt_kernel<D, false>), grid, dim3(256), sizeof(Tile<D, false>), st, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_attn_prompt(const AttnArgs &a, int dtype, int D, int64_t blocks, hipStream_t st) {
+    switch (D) {
+    case 64: return launch_d<64>(a, dtype, blocks, st);
+    case 96: return launch_d<96>(a, dtype, blocks, st);
+    case 128: return launch_d<128>(a, dtype, blocks, st);
+    case 192: return launch_d<192>(a, dtype, blocks, st);
+    case 256: return launch_d<256>(a, dtype, blocks, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qmm

@@ -579,7 +579,8 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
  * j is visible to the token with index i if it has a page, j < lens[s], and, with
  * causal, j <= i, and, with a window w > 0, j > i - w.  A row that sees nothing
  * gets zeros, whatever the cache holds; what a row does not see does not reach
- * it, infinities and NaN neither.
+ * it, infinities and NaN neither.  An infinity that it does see (query, key or
+ * value) may come out as NaN, and an infinite key as NaN where its score would be -infinity.
  * Queries and probabilities are split in two f16 parts under a power of two and
  * multiplied on the matrix cores, f32 accumulation, statistics in f32: f32 class.
  * With S_j = |scale| sum_d |q_d key_jd|, the error of a score is at most

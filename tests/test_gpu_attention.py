@@ -161,8 +161,22 @@ MORE = [
 ]
 
 
-@pytest.mark.parametrize("kw", FEW + MORE, ids=name)
-def test_few_tokens_match_the_softmax(kw):
+MANY = [dict(dtype=dt, Hq=G * Hk, Hk=Hk, D=D, page=page, lens=lens, new=new, **kw)
+        for dt in (1, 8)
+        for D, Hk, G, page, lens, new, kw in (
+            (128, 2, 4, 64, [200], 200, {}), (64, 1, 3, 16, [133, 75], 75, {}), (96, 2, 1, 32, [97, 400], 97, {}),
+            (192, 1, 2, 128, [150], 150, {}), (256, 1, 2, 16, [90, 300], 41, {}), (128, 1, 4, 32, [1500], 40, {}),
+            (64, 2, 1, 16, [300, 170, 41], 160, dict(starts=[2, 162, 162, 203], rows=210)),
+            (64, 2, 4, 64, [600], 100, dict(window=70)), (128, 1, 1, 16, [260, 33], 60, dict(window=1)),
+            (96, 1, 40, 16, [77, 200, 5], 2, dict(causal=False)), (64, 1, 4, 256, [70, 900], 50, dict(causal=False)),
+            (64, 1, 2, 16, [100], 70, dict(cap=10.0)), (128, 1, 2, 16, [100], 70, dict(scale=-0.2)),
+            (64, 1, 2, 16, [100], 70, dict(scale=0.0)), (64, 1, 2, 64, [100], 70, dict(scale=-0.1, cap=4.0)),
+            (128, 2, 1, 64, [20, 64, 1], 64, {}), (64, 1, 2, 32, [150], 60, dict(q_scale=40.0)),
+            (128, 1, 2, 64, [333], 333, dict(pad=32)))]
+
+
+@pytest.mark.parametrize("kw", FEW + MORE + MANY, ids=name)
+def test_attention_matches_the_softmax(kw):
     c = Case(**kw).buffers()
     c.call()
     torch.cuda.synchronize()
@@ -176,7 +190,7 @@ def test_few_tokens_match_the_softmax(kw):
 
 
 @pytest.mark.parametrize("dtype", [1, 8])
-@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("new", [1, 6, 40])
 def test_rows_that_see_nothing(dtype, new):
     """Empty and negative lengths, fewer tokens than rows, pages that are none."""
     c = Case(dtype, 4, 2, 64, 16, [0, -7, 3, 50, 90, 2000], new, max_pages=8, seed=1)
@@ -196,7 +210,7 @@ def test_window_without_pages_sees_nothing():
 
 
 @pytest.mark.parametrize("dtype", [1, 8])
-@pytest.mark.parametrize("new,window", [(4, 0), (4, 3), (8, 0)])
+@pytest.mark.parametrize("new,window", [(4, 0), (4, 3), (8, 0), (37, 0), (37, 20)])
 def test_what_a_row_does_not_see_does_not_reach_it(dtype, new, window):
     """A NaN or infinity in the key and value of one new token: rows that see it are
     what the formula says, not finite; rows that do not are what they were."""
@@ -230,19 +244,24 @@ def test_what_a_row_does_not_see_does_not_reach_it(dtype, new, window):
                     o = c.out[n].view(4, 64)
                     assert not torch.isfinite(o[:, :32]).all() and torch.equal(o[:, 32:], clean.out[n].view(4, 64)[:, 32:])
                 else:
-                    assert not torch.isfinite(c.out[n]).all()
+                    # a NaN score leaves nothing finite; an infinite key's may be of either
+                    # sign (no share, or NaN), or NaN itself where its terms differ in sign
+                    o = torch.isnan(c.out[n].view(4, 64))
+                    assert o.all() if np.isnan(bad) else (o.all(1) | torch.isfinite(c.out[n].view(4, 64)).all(1)).all()
 
 
-def test_nan_query_stays_in_its_row():
-    c = Case(1, 8, 2, 128, 32, [300, 90], 2, seed=4).buffers()
+@pytest.mark.parametrize("dtype", [1, 8])
+@pytest.mark.parametrize("new", [2, 30])
+def test_nan_query_stays_in_its_row(dtype, new):
+    c = Case(dtype, 8, 2, 128, 32, [300, 90], new, seed=4).buffers()
     c.call()
     want = c.out.clone()
     c.d_q[1, 130] = float("nan")
     c.d_q[2, 5] = float("inf")
     c.call()
     torch.cuda.synchronize()
-    got, want = c.out.view(4, 8, 128), want.view(4, 8, 128)
-    hit = torch.zeros(4, 8, dtype=torch.bool)
+    got, want = c.out.view(2 * new, 8, 128), want.view(2 * new, 8, 128)
+    hit = torch.zeros(2 * new, 8, dtype=torch.bool)
     hit[1, 1] = hit[2, 0] = True
     assert torch.isnan(got[hit.cuda()]).all() and torch.equal(got[~hit.cuda()], want[~hit.cuda()])
 
@@ -272,7 +291,7 @@ def test_large_offsets(dtype):
     c.check()
 
 
-@pytest.mark.parametrize("new", [1, 5])
+@pytest.mark.parametrize("new", [1, 5, 20])
 def test_captured_call_follows_the_lengths(new):
     """Two captured calls, each with its own work, replayed together on two
     streams while lengths change between replays."""
