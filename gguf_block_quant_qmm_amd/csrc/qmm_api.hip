@@ -185,7 +185,7 @@ int check_kv(const qmm_kv_cache *c, const qmm_kv_batch *b) {
     if (!kv_sizes_ok(c->pages, c->page, c->heads, c->dim)) return QMM_ERR_SHAPE;
     if (b->seqs < 1 || b->seqs > 65535 || b->max_new < 1 || b->max_new > INT32_MAX / b->seqs) return QMM_ERR_SHAPE;
     if (b->rows < 1 || b->rows > INT32_MAX || (!b->starts && b->rows < b->seqs * b->max_new)) return QMM_ERR_SHAPE;
-    if (b->max_pages < 1 || b->max_pages > INT32_MAX / c->page) return QMM_ERR_SHAPE;
+    if (b->max_pages < 1 || b->max_pages > (int64_t(1) << 30) / c->page) return QMM_ERR_SHAPE;
     if (b->table_stride != 0 && (b->table_stride < b->max_pages || b->table_stride > (int64_t(1) << 40)))
         return QMM_ERR_SHAPE;
     return QMM_OK;

@@ -47,119 +47,153 @@ template <int D> struct Regs<D, true> {
     half8 ks[D / 32], vs[D / 32];  // scales of tokens 8g .. 8g+7
 };
 
-// Where a lane's tokens of a chunk lie: the token whose key it loads is in group
+// The pages of a lane's tokens of a chunk: the token whose key it loads is in group
 // r / 4 of 8 (r = lane % 16), its values' and scores' tokens are group g = lane / 16.
+// -1: the group has none; it reads page 0 and is masked.
 struct Where {
-    const uint8_t *k;   // record with the keys
-    const uint8_t *ks;  // record with the scales of group g's keys (Q8_0)
-    const uint8_t *v;   // record with the values of group g
-    int kslot, slot;
-    bool good;          // group g has a page
+    int k, v;
 };
 
-template <bool Q8>
-__device__ __forceinline__ Where where(const AttnArgs &a, int s, int h, int64_t k0, int64_t rec) {
-    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int64_t kk = k0 + 8 * (r >> 2), kv = k0 + 8 * g;
-    const int pk = kv_page(a.kv, s, kk), pv = kv_page(a.kv, s, kv);
-    const int mask = (1 << a.kv.page_shift) - 1;
-    Where w;
-    w.good = pv >= 0;
-    // a group without a page reads page 0 and is masked
-    const int64_t ok = ((int64_t)(pk < 0 ? 0 : pk) * a.kv.heads + h) * rec, ov = ((int64_t)(pv < 0 ? 0 : pv) * a.kv.heads + h) * rec;
-    w.k = a.kv.k + ok;
-    w.ks = a.kv.k + ov;
-    w.v = a.kv.v + ov;
-    w.kslot = ((int)kk & mask) + (r & 3);
-    w.slot = (int)kv & mask;
-    return w;
+__device__ __forceinline__ Where where(const Pages &page_of, int k0) {
+    const int lane = (int)threadIdx.x & 63;
+    return Where{page_of(k0 + 8 * ((lane & 15) >> 2)), page_of(k0 + 8 * (lane >> 4))};
+}
+
+__device__ __forceinline__ const uint8_t *record_of(const AttnArgs &a, const uint8_t *pool, int page, int h, int64_t rec) {
+    return pool + ((int64_t)(page < 0 ? 0 : page) * a.kv.heads + h) * rec;
 }
 
 template <int D, bool Q8>
-__device__ __forceinline__ void load_keys(const AttnArgs &a, const Where &w, Regs<D, Q8> &x) {
-    const int g = ((int)threadIdx.x & 63) >> 4, page = 1 << a.kv.page_shift;
+__device__ __forceinline__ void load_keys(const AttnArgs &a, const Where &w, int h, int k0, int64_t rec, Regs<D, Q8> &x) {
+    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4, page = 1 << a.kv.page_shift;
+    const uint8_t *p = record_of(a, a.kv.k, w.k, h, rec);
+    const int slot = ((k0 + 8 * (r >> 2)) & (page - 1)) + (r & 3);
 #pragma unroll
     for (int t = 0; t < 2; t++)
 #pragma unroll
         for (int b = 0; b < D / 32; b++) {
-            const int at = (w.kslot + 4 * t) * D + 32 * b + 8 * g;
-            if constexpr (Q8) x.k[t][b] = *reinterpret_cast<const u32x2_t *>(w.k + at);
-            else x.k[t][b] = *reinterpret_cast<const u32x4_t *>(w.k + 2 * at);
+            const int at = (slot + 4 * t) * D + 32 * b + 8 * g;
+            if constexpr (Q8) x.k[t][b] = *reinterpret_cast<const u32x2_t *>(p + at);
+            else x.k[t][b] = *reinterpret_cast<const u32x4_t *>(p + 2 * at);
         }
     if constexpr (Q8) {
+        const uint8_t *ps = record_of(a, a.kv.k, w.v, h, rec) + page * D;
+        const int s0 = (k0 + 8 * g) & (page - 1);
 #pragma unroll
-        for (int b = 0; b < D / 32; b++)
-            x.ks[b] = *reinterpret_cast<const half8 *>(w.ks + page * D + 2 * (b * page + w.slot));
+        for (int b = 0; b < D / 32; b++) x.ks[b] = *reinterpret_cast<const half8 *>(ps + 2 * (b * page + s0));
     }
 }
 
 template <int D, bool Q8>
-__device__ __forceinline__ void load_values(const AttnArgs &a, const Where &w, Regs<D, Q8> &x) {
-    const int r = (int)threadIdx.x & 15, page = 1 << a.kv.page_shift;
+__device__ __forceinline__ void load_values(const AttnArgs &a, const Where &w, int h, int k0, int64_t rec, Regs<D, Q8> &x) {
+    const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4, page = 1 << a.kv.page_shift;
+    const uint8_t *p = record_of(a, a.kv.v, w.v, h, rec);
+    const int slot = (k0 + 8 * g) & (page - 1);
 #pragma unroll
     for (int d = 0; d < D / 16; d++) {
-        const int at = (16 * d + r) * page + w.slot;
-        if constexpr (Q8) x.v[d] = *reinterpret_cast<const u32x2_t *>(w.v + at);
-        else x.v[d] = *reinterpret_cast<const u32x4_t *>(w.v + 2 * at);
+        const int at = (16 * d + r) * page + slot;
+        if constexpr (Q8) x.v[d] = *reinterpret_cast<const u32x2_t *>(p + at);
+        else x.v[d] = *reinterpret_cast<const u32x4_t *>(p + 2 * at);
     }
     if constexpr (Q8) {
 #pragma unroll
         for (int b = 0; b < D / 32; b++)
-            x.vs[b] = *reinterpret_cast<const half8 *>(w.v + page * D + 2 * (b * page + w.slot));
+            x.vs[b] = *reinterpret_cast<const half8 *>(p + page * D + 2 * (b * page + slot));
     }
 }
 
 // MODE 0: up to 8 rows a workgroup, both parts in one column tile; 1, 2: one or
 // two tiles of 16 rows, each part its own product.
 template <int D, bool Q8, int MODE>
-__global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * kWaves, MODE == 0 && D <= 128 ? 3 : D <= 128 ? 2 : 1) attn_few_kernel(const AttnArgs a) {
     constexpr int NC = MODE == 0 ? 1 : MODE, RT = MODE == 0 ? 8 : 16 * MODE, NK = D / 32, ND = D / 16;
     constexpr bool STACK = MODE == 0;
     __shared__ __attribute__((aligned(16))) float lo_[kWaves][16][D + 4];
     __shared__ float2 lstat[kWaves][NC * 16];
+    __shared__ half8 lq[STACK ? 1 : NC][STACK ? 1 : NK][2][STACK ? 1 : 64];
+    __shared__ float lmul[STACK ? 1 : NC][16];
     AttnShare w;
     if (!attn_share<RT, kChunk>(a, kLeast, w)) return;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int64_t rec = kv_record(Q8 ? QMM_Q8_0 : QMM_F16, (int64_t)1 << a.kv.page_shift, D);
 
-    // the queries' two parts, and what each of the lane's columns sees
-    half8 qh[NC][NK], ql[NC][NK];
+    const Pages page_of(a, w.s);
+    int k0 = w.k0 + kChunk * wave;
+    Regs<D, Q8> x;
+    Where at{}, next{};
+    if (k0 < w.k1) at = where(page_of, k0);
+
+    // the queries' two parts (one tile: in registers, every wavefront its own; more rows:
+    // in LDS, made by a wavefront a tile), and what each of the lane's columns sees
+    half8 qf[STACK ? NK : 1];
     float mul[NC];
-    int64_t lo[NC], hi[NC];
+    int lo[NC], hi[NC];
+    int row[NC];
 #pragma unroll
     for (int c = 0; c < NC; c++) {
         const int r = STACK ? (col & 7) : 16 * c + col;
         const bool on = r < w.nrows;
-        const int row = w.r0 + (on ? r : 0), t = row / a.G, hq = w.h * a.G + (row - t * a.G);
-        attn_sees(a, w.nw, t, lo[c], hi[c]);
+        row[c] = w.r0 + (on ? r : 0);
+        attn_sees(a, w.nw, row[c] / a.G, lo[c], hi[c]);
         if (!on) lo[c] = hi[c] = 0;
+    }
+    auto queries = [&](int c, auto put) {
+        const int t = row[c] / a.G, hq = w.h * a.G + (row[c] - t * a.G);
+        const bool on = (STACK ? (col & 7) : 16 * c + col) < w.nrows;
         const float *q = a.Q + (int64_t)(w.nw.first + t) * a.q_stride + (int64_t)hq * D + 8 * g;
-        floatx4 x[NK][2];
+        floatx4 y[NK][2];
+#pragma unroll
+        for (int b = 0; b < NK; b++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) y[b][i] = *reinterpret_cast<const floatx4 *>(q + 32 * b + 4 * i);
+        // the first chunk is asked for before the queries are looked at
+        if (c == 0 && k0 < w.k1) {
+            load_keys<D, Q8>(a, at, w.h, k0, rec, x);
+            load_values<D, Q8>(a, at, w.h, k0, rec, x);
+        }
         float amax = 0.f;
 #pragma unroll
         for (int b = 0; b < NK; b++)
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                x[b][i] = *reinterpret_cast<const floatx4 *>(q + 32 * b + 4 * i);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    if (!on) x[b][i][j] = 0.f;
-                    amax = fmaxf(amax, fabsf(x[b][i][j]));
-                }
+            for (int i = 0; i < 8; i++) {
+                if (!on) y[b][i / 4][i % 4] = 0.f;
+                amax = fmaxf(amax, fabsf(y[b][i / 4][i % 4]));
             }
-        amax = fold32(fold16(amax, MaxOp()), MaxOp());
-        const int e = row_exponent(amax);
-        mul[c] = attn_mul(a, e);
+        const int e = row_exponent(fold32(fold16(amax, MaxOp()), MaxOp()));
 #pragma unroll
-        for (int b = 0; b < NK; b++)
+        for (int b = 0; b < NK; b++) {
+            half8 p, rest;
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float v = ldexpf(x[b][i / 4][i % 4], e);
-                const _Float16 p = (_Float16)v, rest = (_Float16)(v - (float)p);
-                qh[c][b][i] = STACK && col >= 8 ? rest : p;
-                ql[c][b][i] = rest;
+                const float v = ldexpf(y[b][i / 4][i % 4], e);
+                p[i] = (_Float16)v;
+                rest[i] = (_Float16)(v - (float)p[i]);
             }
+            put(b, p, rest);
+        }
+        return attn_mul(a, e);
+    };
+    if constexpr (STACK) {
+        mul[0] = queries(0, [&](int b, half8 p, half8 rest) { qf[b] = col >= 8 ? rest : p; });
+    } else {
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            if (wave == c) {
+                const float m_ = queries(c, [&](int b, half8 p, half8 rest) {
+                    lq[c][b][0][lane] = p;
+                    lq[c][b][1][lane] = rest;
+                });
+                if (g == 0) lmul[c][col] = m_;
+            }
+        }
+        if (wave != 0 && k0 < w.k1) {
+            load_keys<D, Q8>(a, at, w.h, k0, rec, x);
+            load_values<D, Q8>(a, at, w.h, k0, rec, x);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < NC; c++) mul[c] = lmul[c][col];
     }
 
     floatx4 o[NC][ND];
@@ -174,62 +208,77 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
         for (int d = 0; d < ND; d++) o[c][d] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
 
-    Regs<D, Q8> x;
-    int64_t k0 = w.k0 + kChunk * wave;
-    Where at{}, next{};
-    if (k0 < w.k1) {
-        at = where<Q8>(a, w.s, w.h, k0, rec);
-        load_keys<D, Q8>(a, at, x);
-        load_values<D, Q8>(a, at, x);
-    }
     for (; k0 < w.k1; k0 += kChunk * kWaves) {
-        const int64_t kn = k0 + kChunk * kWaves;
-        if (kn < w.k1) next = where<Q8>(a, w.s, w.h, kn, rec);
+        const int kn = k0 + kChunk * kWaves;
+        if (kn < w.k1) next = where(page_of, kn);
         // scores: s[c][4 t + i] is token k0 + 8 g + 4 t + i of column c
         float s[NC][8];
+        {
+            floatx4 sum[2][NC];
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            floatx4 sum[NC];
+            for (int t = 0; t < 2; t++)
 #pragma unroll
-            for (int c = 0; c < NC; c++) sum[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+                for (int c = 0; c < NC; c++) sum[t][c] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int b = 0; b < NK; b++) {
-                half8 kf;
-                if constexpr (Q8) kf = codes8(x.k[t][b]);
-                else kf = __builtin_bit_cast(half8, x.k[t][b]);
+                half8 kf[2];
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    if constexpr (Q8) kf[t] = codes8(x.k[t][b]);
+                    else kf[t] = __builtin_bit_cast(half8, x.k[t][b]);
+                }
 #pragma unroll
                 for (int c = 0; c < NC; c++) {
-                    floatx4 z = Q8 ? floatx4{0.f, 0.f, 0.f, 0.f} : sum[c];
-                    if constexpr (!STACK) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, ql[c][b], z, 0, 0, 0);
-                    z = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qh[c][b], z, 0, 0, 0);
-                    if constexpr (Q8) {
-#pragma unroll
-                        for (int i = 0; i < 4; i++) sum[c][i] = fmaf(z[i], (float)x.ks[b][4 * t + i], sum[c][i]);
+                    half8 qh, ql;
+                    if constexpr (STACK) {
+                        qh = qf[b];
                     } else {
-                        sum[c] = z;
+                        qh = lq[c][b][0][lane];
+                        ql = lq[c][b][1][lane];
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        floatx4 z = Q8 ? floatx4{0.f, 0.f, 0.f, 0.f} : sum[t][c];
+                        if constexpr (!STACK) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[t], ql, z, 0, 0, 0);
+                        z = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[t], qh, z, 0, 0, 0);
+                        if constexpr (Q8) {
+#pragma unroll
+                            for (int i = 0; i < 4; i++) sum[t][c][i] = fmaf(z[i], (float)x.ks[b][4 * t + i], sum[t][c][i]);
+                        } else {
+                            sum[t][c] = z;
+                        }
                     }
                 }
+                if constexpr (Q8) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int c = 0; c < NC; c++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    float v = sum[c][i];
-                    if constexpr (STACK)  // the other part's column: row_ror 8
-                        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
-                    s[c][4 * t + i] = attn_score(v, mul[c], a.softcap);
-                }
+                for (int t = 0; t < 2; t++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        float v = sum[t][c][i];
+                        if constexpr (STACK)  // the other part's column: row_ror 8
+                            v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
+                        s[c][4 * t + i] = v * mul[c];
+                    }
+            if (a.softcap > 0.f) {  // uniform
+#pragma unroll
+                for (int c = 0; c < NC; c++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) s[c][j] = capped(s[c][j], a.softcap);
+            }
         }
-        if (kn < w.k1) load_keys<D, Q8>(a, next, x);
+        if (kn < w.k1) load_keys<D, Q8>(a, next, w.h, kn, rec, x);
 
-        const bool plain = k0 >= w.lo_all && k0 + kChunk <= w.hi_all && __ballot(!at.good) == 0;  // uniform
+        const bool plain = k0 >= w.lo_all && k0 + kChunk <= w.hi_all && __ballot(at.v < 0) == 0;  // uniform
         if (!plain) {
 #pragma unroll
             for (int c = 0; c < NC; c++)
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    const int64_t k = k0 + 8 * g + j;
-                    if (!at.good || k < lo[c] || k >= hi[c]) s[c][j] = -INFINITY;
+                    const int k = k0 + 8 * g + j;
+                    if (at.v < 0 || k < lo[c] || k >= hi[c]) s[c][j] = -INFINITY;
                 }
         }
         // what no row sees has no value, whatever the pool holds there.  What
@@ -239,11 +288,15 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
         if (!plain) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const int64_t k = k0 + 8 * g + j;
-                const bool any = at.good && k >= w.lo_any && k < w.hi_any, all = at.good && k >= w.lo_all && k < w.hi_all;
+                const int k = k0 + 8 * g + j;
+                const bool any = at.v >= 0 && k >= w.lo_any && k < w.hi_any, all = at.v >= 0 && k >= w.lo_all && k < w.hi_all;
                 if constexpr (Q8) {
 #pragma unroll
-                    for (int b = 0; b < NK; b++) x.vs[b][j] = any ? x.vs[b][j] : (_Float16)0.f;
+                    for (int b = 0; b < NK; b++) {
+                        const bool inf = !__builtin_isfinite((float)x.vs[b][j]);
+                        odd |= inf && any && !all;
+                        if (!any || (inf && !all)) x.vs[b][j] = (_Float16)0.f;
+                    }
                 } else {
                     const uint32_t sel = j & 1 ? 0xFFFF0000u : 0x0000FFFFu, exps = sel & 0x7C007C00u;
 #pragma unroll
@@ -256,30 +309,37 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
                 }
             }
         }
-        // 2^15: the f16 parts of a probability below 2^-14 keep their bits.  Q8_0: under the
-        // power of two that the finite value scales the row has seen stay below,
-        // |scale| < 2^(top - 14)
+        // f16: probabilities are 2^15 times themselves, so that both parts of one below
+        // 2^-14 keep their bits.  Q8_0: a probability times its token's value scale,
+        // under the power of two that the scales the row has seen stay below, |scale| < 2^(top - 14)
         float grow[NC], unit[NC];
         if constexpr (Q8) {
-            uint32_t es[8];
+            typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+            ushort2_t es[4];  // tokens 2i and 2i + 1: the largest scale's bits
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                es[j] = 0;
+            for (int i = 0; i < 4; i++) {
+                es[i] = ushort2_t{0, 0};
 #pragma unroll
                 for (int b = 0; b < NK; b++) {
-                    const _Float16 sc = x.vs[b][j];  // a bit cast of the element itself reads element 0
-                    const uint32_t u = __builtin_bit_cast(uint16_t, sc) & 0x7FFFu;
-                    es[j] = u > es[j] && u < 0x7C00u ? u : es[j];
+                    const u32x4_t v = __builtin_bit_cast(u32x4_t, x.vs[b]);
+                    const uint32_t u = v[i] & 0x7FFF7FFFu;
+                    es[i] = __builtin_elementwise_max(es[i], __builtin_bit_cast(ushort2_t, u));
                 }
             }
 #pragma unroll
             for (int c = 0; c < NC; c++) {
-                uint32_t e = 0;
+                uint32_t e;
+                if (plain) {
+                    const ushort2_t m2 = __builtin_elementwise_max(__builtin_elementwise_max(es[0], es[1]), __builtin_elementwise_max(es[2], es[3]));
+                    e = m2.x > m2.y ? m2.x : m2.y;
+                } else {
+                    e = 0;
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const int64_t k = k0 + 8 * g + j;
-                    const uint32_t u = plain || (k >= lo[c] && k < hi[c]) ? es[j] : 0u;
-                    e = u > e ? u : e;
+                    for (int j = 0; j < 8; j++) {
+                        const int k = k0 + 8 * g + j;
+                        const uint32_t u = k >= lo[c] && k < hi[c] ? es[j / 2][j & 1] : 0u;
+                        e = u > e ? u : e;
+                    }
                 }
                 const int now = (int)fold32(fold16((float)(e >> 10), MaxOp()), MaxOp());
                 const int up = now > top[c] ? now : top[c];
@@ -289,10 +349,7 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
             }
         } else {
 #pragma unroll
-            for (int c = 0; c < NC; c++) {
-                grow[c] = 1.f;
-                unit[c] = 32768.f;
-            }
+            for (int c = 0; c < NC; c++) grow[c] = 1.f;
         }
 #pragma unroll
         for (int c = 0; c < NC; c++) {
@@ -300,14 +357,15 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
 #pragma unroll
             for (int j = 1; j < 8; j++) mx = fmaxf(mx, s[c][j]);
             mx = fmaxf(m[c], fold32(fold16(mx, MaxOp()), MaxOp()));
-            const float ref = mx == -INFINITY ? 0.f : mx;
-            const float alpha = __builtin_amdgcn_exp2f(m[c] - ref);
+            const float ref = mx == -INFINITY ? 0.f : mx - (Q8 ? 0.f : 15.f), was = m[c] - (Q8 ? 0.f : 15.f);
+            const float alpha = __builtin_amdgcn_exp2f(was - ref);
             m[c] = mx;
             float ps = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 s[c][j] = __builtin_amdgcn_exp2f(s[c][j] - ref);
                 ps += s[c][j];
+                if constexpr (Q8) s[c][j] *= unit[c];
             }
             l[c] = fmaf(l[c], alpha, ps);
             const float f = alpha * grow[c];
@@ -318,61 +376,72 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
                     for (int i = 0; i < 4; i++) o[c][d][i] *= f;
             }
         }
+        half8 ph[NC], pl[NC];
+        auto parts = [&](int b) {
+#pragma unroll
+            for (int c = 0; c < NC; c++)
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    half2_t h, r;
+                    if constexpr (Q8) split2(s[c][j] * (float)x.vs[b][j], s[c][j + 1] * (float)x.vs[b][j + 1], h, r);
+                    else split2(s[c][j], s[c][j + 1], h, r);
+                    if (STACK) h = col >= 8 ? r : h;
+                    ph[c][j] = h.x, ph[c][j + 1] = h.y;
+                    pl[c][j] = r.x, pl[c][j + 1] = r.y;
+                }
+        };
+        if constexpr (!Q8) parts(0);
 #pragma unroll
         for (int b = 0; b < NK; b++) {
             half8 v0, v1;
             if constexpr (Q8) {
                 v0 = codes8(x.v[2 * b]);
                 v1 = codes8(x.v[2 * b + 1]);
+                parts(b);
             } else {
                 v0 = __builtin_bit_cast(half8, x.v[2 * b]);
                 v1 = __builtin_bit_cast(half8, x.v[2 * b + 1]);
             }
 #pragma unroll
             for (int c = 0; c < NC; c++) {
-                half8 ph, pl;
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    float p = s[c][j] * unit[c];
-                    if constexpr (Q8) p = s[c][j] == 0.f ? 0.f : p * (float)x.vs[b][j];
-                    const _Float16 hi_ = (_Float16)p, rest = (_Float16)(p - (float)hi_);
-                    ph[j] = STACK && col >= 8 ? rest : hi_;
-                    pl[j] = rest;
-                }
                 if constexpr (!STACK) {
-                    o[c][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl, o[c][2 * b], 0, 0, 0);
-                    o[c][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl, o[c][2 * b + 1], 0, 0, 0);
+                    o[c][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pl[c], o[c][2 * b], 0, 0, 0);
+                    o[c][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pl[c], o[c][2 * b + 1], 0, 0, 0);
                 }
-                o[c][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, ph, o[c][2 * b], 0, 0, 0);
-                o[c][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, ph, o[c][2 * b + 1], 0, 0, 0);
+                o[c][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, ph[c], o[c][2 * b], 0, 0, 0);
+                o[c][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, ph[c], o[c][2 * b + 1], 0, 0, 0);
             }
+            // the blocks' conversions one after the other: all at once they spill
+            if constexpr (Q8) __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (!Q8) {
-            if (__ballot(odd)) {  // uniform; rare: an infinity or NaN that only some rows see
-                for (int j = 0; j < kChunk; j++) {
-                    const int64_t k = k0 + j;
-                    const int pg = kv_page(a.kv, w.s, k);
-                    if (pg < 0) continue;
-                    const int page = 1 << a.kv.page_shift;
-                    const _Float16 *v = reinterpret_cast<const _Float16 *>(a.kv.v + ((int64_t)pg * a.kv.heads + w.h) * rec) + ((int)k & (page - 1));
+        if (__ballot(odd)) {  // uniform; rare: an infinity or NaN that only some rows see
+            for (int j = 0; j < kChunk; j++) {
+                const int k = k0 + j, pg = page_of(k);
+                if (pg < 0 || (k >= w.lo_all && k < w.hi_all)) continue;
+                const int page = 1 << a.kv.page_shift, slot = k & (page - 1);
+                const uint8_t *p = record_of(a, a.kv.v, pg, w.h, rec);
 #pragma unroll
-                    for (int d = 0; d < ND; d++)
+                for (int d = 0; d < ND; d++)
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            // addresses made here each time, not kept in registers through the main loop
-                            int dim = 16 * d + 4 * g + i;
-                            asm volatile("" : "+v"(dim));
-                            const float y = (float)v[dim * page];
-                            if (__builtin_isfinite(y) || (k >= w.lo_all && k < w.hi_all)) continue;
+                    for (int i = 0; i < 4; i++) {
+                        // addresses made here each time, not kept in registers through the main loop
+                        int dim = 16 * d + 4 * g + i;
+                        asm volatile("" : "+v"(dim));
+                        float y;
+                        if constexpr (Q8)
+                            y = (float)reinterpret_cast<const int8_t *>(p)[dim * page + slot] *
+                                (float)reinterpret_cast<const _Float16 *>(p + page * D)[(dim >> 5) * page + slot];
+                        else
+                            y = (float)reinterpret_cast<const _Float16 *>(p)[dim * page + slot];
+                        if (__builtin_isfinite(y)) continue;
 #pragma unroll
-                            for (int c = 0; c < NC; c++)
-                                if (k >= lo[c] && k < hi[c]) o[c][d][i] += y;
-                        }
-                }
+                        for (int c = 0; c < NC; c++)
+                            if (k >= lo[c] && k < hi[c]) o[c][d][i] += y;
+                    }
             }
         }
         at = next;
-        if (kn < w.k1) load_values<D, Q8>(a, at, x);
+        if (kn < w.k1) load_values<D, Q8>(a, at, w.h, kn, rec, x);
     }
 
     // join the wavefronts
@@ -380,11 +449,12 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
     for (int c = 0; c < NC; c++) {
         l[c] = fold32(fold16(l[c], SumOp()), SumOp());
         if (l[c] != l[c]) m[c] = INFINITY;  // a NaN score is no maximum, but its row is not one that saw nothing
+        if constexpr (!Q8) m[c] -= 15.f;  // probabilities and sums are 2^15 times theirs
         if (g == 0) lstat[wave][16 * c + col] = make_float2(m[c], l[c]);
     }
 #pragma unroll
     for (int c = 0; c < NC; c++) {
-        const float down = Q8 ? ldexpf(1.f, top[c] - 29) : 1.f / 32768.f;
+        const float down = Q8 ? ldexpf(1.f, top[c] - 29) : 1.f;
         __syncthreads();
         float M = -INFINITY;
 #pragma unroll
@@ -433,35 +503,46 @@ __global__ void __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) attn_few_kernel
 // 2^(m_s - M) l_s.  W wavefronts a row take every W-th split.
 template <int D, int W>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
-    constexpr int NV = (D + 63) / 64;
+    constexpr int NV = (D + 63) / 64, NB = 2;  // at most 64 NB splits
     __shared__ float acc[4][D];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t rh = (a.block0 + blockIdx.x) * (4 / W) + (W == 4 ? 0 : wave);
     if (rh >= (int64_t)a.kv.rows * a.Hq) return;  // W 1: whole wavefronts, no barrier follows
+    // the statistics are asked for before the row is known to be one; a lane a split
+    float2 st[NB];
+#pragma unroll
+    for (int b = 0; b < NB; b++)
+        st[b] = 64 * b + lane < a.splits ? a.stat[rh * a.splits + 64 * b + lane] : make_float2(-INFINITY, 0.f);
     const int n = (int)(rh / a.Hq);
     const int s = kv_row_seq(a.kv, n);
     if (s < 0) return;
     const KvNew nw = kv_new(a.kv, s);
     if (n - nw.first >= nw.count) return;
-    const float2 *st = a.stat + rh * a.splits;
-    const float *part = a.part + rh * a.splits * D;
-    float M = -INFINITY;
-    for (int i = lane; i < a.splits; i += 64) M = fmaxf(M, st[i].x);
+    float M = fmaxf(st[0].x, st[1].x);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
-    float y[NV] = {}, L = 0.f;
-    for (int i = lane; i < a.splits; i += 64)
-        if (st[i].x != -INFINITY) L = fmaf(st[i].y, __builtin_amdgcn_exp2f(st[i].x - M), L);
+    for (int o = 1; o < 64; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+    float f[NB], L = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+        f[b] = st[b].x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st[b].x - M);
+        L += f[b] == 0.f ? 0.f : st[b].y * f[b];
+    }
     L = wave_sum(L);
-    const int w0 = W == 4 ? wave : 0;
-#pragma unroll 4
-    for (int i = w0; i < a.splits; i += W) {
-        const float mi = st[i].x;
-        if (mi == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(mi - M);
+    const float *part = a.part + rh * a.splits * D;
+    float y[NV] = {};
 #pragma unroll
-        for (int v = 0; v < NV; v++)
-            if (64 * v + lane < D) y[v] = fmaf(part[(int64_t)i * D + 64 * v + lane], f, y[v]);
+    for (int b = 0; b < NB; b++) {
+        const int i1 = a.splits - 64 * b < 64 ? a.splits - 64 * b : 64;
+#pragma unroll 8
+        for (int i = W == 4 ? wave : 0; i < i1; i += W) {
+            const float fi = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f[b]), i));
+#pragma unroll
+            for (int v = 0; v < NV; v++) {
+                // a split that saw nothing wrote nothing: what lies there may be NaN
+                const float p = 64 * v + lane < D ? part[(int64_t)(64 * b + i) * D + 64 * v + lane] : 0.f;
+                y[v] += fi == 0.f ? 0.f : p * fi;
+            }
+        }
     }
     if constexpr (W == 4) {
 #pragma unroll
@@ -492,10 +573,24 @@ Plan plan_of(const qmm_kv_cache &c, const qmm_kv_batch &b, int64_t q_heads) {
     p.mode = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
     const int64_t rt = p.mode == 0 ? 8 : p.mode == 3 ? kPromptRows : 16 * p.mode;
     p.tiles = (int)((rows + rt - 1) / rt);
-    const int64_t least = p.mode == 3 ? 4 * kPromptChunk : 2 * kLeast * kChunk;  // tokens of a split
-    const int64_t want = (512 + units * p.tiles - 1) / (units * p.tiles), most = (b.max_pages * c.page + least - 1) / least;
-    const int64_t s = want < most ? want : most;
-    p.splits = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+    const int64_t groups = units * p.tiles, tokens = b.max_pages * c.page;
+    // so many splits that there are `total` workgroups, of at least `least` tokens each
+    auto share = [&](int64_t total, int64_t least) {
+        const int64_t want = (total + groups - 1) / groups, most = (tokens + least - 1) / least;
+        return want < most ? want : most;
+    };
+    int64_t s;
+    if (p.mode == 3) {
+        s = share(tuning_lever("QMM_ATTN_PROMPT_GROUPS", 512), tuning_lever("QMM_ATTN_PROMPT_LEAST", 256));
+    } else {
+        const int64_t wide = share(tuning_lever("QMM_ATTN_FILL", 256), tuning_lever("QMM_ATTN_FILL_LEAST", 128)),
+                      even = share(tuning_lever("QMM_ATTN_GROUPS", 4096), tuning_lever("QMM_ATTN_LEAST", 512));
+        const int64_t most = tuning_lever("QMM_ATTN_SPLITS", 32);  // for the balance: each costs the join a read
+        s = even < most ? even : most;
+        s = wide > s ? wide : s;
+    }
+    const int64_t cap = 128;  // what the join holds
+    p.splits = (int)(s < 1 ? 1 : s > cap ? cap : s);
     p.blocks = units * p.tiles * p.splits;
     return p;
 }

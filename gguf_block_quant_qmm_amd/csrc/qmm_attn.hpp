@@ -28,18 +28,19 @@ struct AttnArgs {
 struct AttnShare {
     KvNew nw;
     int s, h, split, r0, nrows;
-    int64_t lo_any, hi_any;  // seen by some row of the tile: lo_any <= j < hi_any
-    int64_t lo_all, hi_all;  // seen by every row (where the pages exist)
-    int64_t k0, k1;
+    int lo_any, hi_any;  // seen by some row of the tile: lo_any <= j < hi_any
+    int lo_all, hi_all;  // seen by every row (where the pages exist)
+    int k0, k1;
 };
 
-__device__ __forceinline__ void attn_sees(const AttnArgs &a, const KvNew &nw, int t, int64_t &lo, int64_t &hi) {
+// What new token t sees: lo <= j < hi.  A table reaches no further than token 2^30.
+__device__ __forceinline__ void attn_sees(const AttnArgs &a, const KvNew &nw, int t, int &lo, int &hi) {
     const int64_t i = nw.index + t, cap = (int64_t)a.kv.max_pages << a.kv.page_shift;
-    hi = a.causal && i + 1 < nw.len ? i + 1 : nw.len;
-    hi = hi < cap ? hi : cap;
-    hi = hi > 0 ? hi : 0;
-    lo = a.window && i - a.window + 1 > 0 ? i - a.window + 1 : 0;
-    lo = lo < hi ? lo : hi;
+    int64_t to = a.causal && i + 1 < nw.len ? i + 1 : nw.len;
+    to = to < cap ? to : cap;
+    hi = (int)(to > 0 ? to : 0);
+    const int64_t from = a.window && i - a.window + 1 > 0 ? i - a.window + 1 : 0;
+    lo = (int)(from < hi ? from : hi);
 }
 
 // False if the workgroup has no rows.  CH: tokens of a chunk; a split takes at
@@ -65,19 +66,32 @@ __device__ __forceinline__ bool attn_share(const AttnArgs &a, int least, AttnSha
     if (r0 >= rows) return false;
     w.r0 = (int)r0;
     w.nrows = (int)(rows - r0 < RT ? rows - r0 : RT);
-    int64_t lo1, hi1;
+    int lo1, hi1;
     attn_sees(a, w.nw, w.r0 / a.G, w.lo_any, w.hi_all);
     attn_sees(a, w.nw, (w.r0 + w.nrows - 1) / a.G, lo1, hi1);
     w.hi_any = hi1;
     w.lo_all = lo1;
-    const int64_t c0 = w.lo_any / CH, c1 = (w.hi_any + CH - 1) / CH;
-    int64_t per = (c1 - c0 + a.splits - 1) / a.splits;
+    const int c0 = w.lo_any / CH, c1 = (w.hi_any + CH - 1) / CH;
+    int per = (c1 - c0 + a.splits - 1) / a.splits;
     per = per > least ? per : least;
-    const int64_t b0 = c0 + per * w.split, b1 = b0 + per;
-    w.k0 = b0 * CH;
-    w.k1 = (b1 < c1 ? b1 : c1) * CH;
+    const int64_t b0 = c0 + (int64_t)per * w.split, b1 = b0 + per;
+    w.k0 = (int)(b0 < c1 ? b0 : c1) * CH;
+    w.k1 = (int)(b1 < c1 ? b1 : c1) * CH;
     return true;
 }
+
+// A sequence's row of the page table; token i's page (0 <= i <= 2^30 + 64), or -1.
+struct Pages {
+    const int32_t *row;
+    int shift, columns, pages;
+    __device__ __forceinline__ Pages(const AttnArgs &a, int s)
+        : row(a.kv.table + (int64_t)s * a.kv.table_stride), shift(a.kv.page_shift), columns(a.kv.max_pages), pages(a.kv.pages) {}
+    __device__ __forceinline__ int operator()(int i) const {
+        const int c = i >> shift;
+        const int p = c < columns ? row[c] : -1;
+        return (uint32_t)p < (uint32_t)pages ? p : -1;
+    }
+};
 
 // The value of the other half of the wavefront (lane ^ 32), and of the neighbouring row of
 // 16 lanes (lane ^ 16), folded into v by `op`.
@@ -110,13 +124,24 @@ __device__ __forceinline__ int row_exponent(float amax) {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Scores in base 2 from the raw products: mul is scale * 2^-e * log2(e), or,
-// under a softcap, scale * 2^-e / softcap.
-__device__ __forceinline__ float attn_score(float raw, float mul, float softcap) {
-    return softcap > 0.f ? softcap * kLog2e * tanhf(raw * mul) : raw * mul;
-}
+// A raw product times this is the score in base 2, or, under a softcap, the
+// argument of capped().
 __device__ __forceinline__ float attn_mul(const AttnArgs &a, int e) {
     return ldexpf(a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e, -e);
+}
+__device__ __forceinline__ float capped(float x, float softcap) { return softcap * kLog2e * tanhf(x); }
+
+// p = hi + lo in f16 to 2^-23 of p (2^-25 near 0): two conversions for two values and one FMA
+// that reads its f16 operand as it is for each rest (p - hi, exact).  The rests
+// come after the conversions of the same values, so no wait of a value's own producer is
+// left to them.
+__device__ __forceinline__ void split2(float p0, float p1, half2_t &hi, half2_t &lo) {
+    typedef float float2_t __attribute__((ext_vector_type(2)));
+    hi = __builtin_convertvector((float2_t{p0, p1}), half2_t);
+    float r0, r1;
+    asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r0) : "v"(hi), "v"(p0));
+    asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r1) : "v"(hi), "v"(p1));
+    lo = __builtin_convertvector((float2_t{r0, r1}), half2_t);
 }
 
 // Four codes of a dword as f16 pairs, exactly: byte ^ 0x80 is code + 128, under

@@ -60,7 +60,7 @@ template <int D, bool Q8> struct Tile {  // in LDS
 __device__ __forceinline__ int swap23(int t) { return (t & ~12) | ((t & 4) << 1) | ((t & 8) >> 1); }
 
 // A token's distance from the tile's first, cut to what the tile can tell apart.
-__device__ __forceinline__ int within(int64_t x) { return (int)(x < 0 ? 0 : x > CH ? CH : x); }
+__device__ __forceinline__ int within(int x) { return x < 0 ? 0 : x > CH ? CH : x; }
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(const AttnArgs a) {
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
     const int r = 32 * wave + col;
     const bool on = r < w.nrows, wave_on = 32 * wave < w.nrows;
     const int row = w.r0 + (on ? r : 0), t = row / a.G, hq = w.h * a.G + (row - t * a.G);
-    int64_t lo, hi;
+    int lo, hi;
     attn_sees(a, w.nw, t, lo, hi);
     if (!on) lo = hi = 0;
 
@@ -123,21 +123,15 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
     Stage<D, Q8> st;
     int good = 0;  // which of the tile's four runs of 16 tokens have a page
     const int g = lane & 7, d0 = wave * (D / 4) + (lane >> 3);  // the values' tokens 8g .. 8g+7 and dims d0 + 8i
-    auto load = [&](int64_t k0) {
-        int pg[4];
-        good = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            pg[i] = __builtin_amdgcn_readfirstlane(kv_page(a.kv, w.s, k0 + 16 * i));
-            good |= (pg[i] >= 0) << i;
-            pg[i] = pg[i] < 0 ? 0 : pg[i];  // masked
-        }
-        auto record = [&](int run) {
-            const int p01 = run & 1 ? pg[1] : pg[0], p23 = run & 1 ? pg[3] : pg[2];
-            return ((int64_t)(run & 2 ? p23 : p01) * a.kv.heads + w.h) * rec;
-        };
-        const uint8_t *kr = a.kv.k + record(wave);
-        const int kslot = (int)(k0 + 16 * wave) & (page - 1);
+    const Pages page_of(a, w.s);
+    int pg = page_of(w.k0 + 16 * (lane & 3));  // lane r % 4: the page of the next tile's run r
+    auto load = [&](int k0) {
+        good = (int)__ballot(pg >= 0) & 15;
+        const int at = pg < 0 ? 0 : pg;  // masked
+        const uint8_t *kr = a.kv.k + ((int64_t)__builtin_amdgcn_readlane(at, wave) * a.kv.heads + w.h) * rec;
+        const int pv = __shfl(at, g >> 1, 64);
+        const uint8_t *vr = a.kv.v + ((int64_t)pv * a.kv.heads + w.h) * rec;
+        const int kslot = (k0 + 16 * wave) & (page - 1);
 #pragma unroll
         for (int i = 0; i < NS; i++) {
             if constexpr (Q8) st.k[i] = *reinterpret_cast<const u32x2_t *>(kr + kslot * D + 8 * lane + 512 * i);
@@ -146,12 +140,11 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         if constexpr (Q8) {
             if (tid < 16 * NS) {
                 const int b = tid >> 4, key = 4 * (tid & 15);
-                const uint8_t *p = a.kv.k + record(key >> 4) + page * D;
-                st.ks = *reinterpret_cast<const u32x2_t *>(p + 2 * (b * page + ((int)(k0 + key) & (page - 1))));
+                const uint8_t *p = a.kv.k + ((int64_t)__shfl(at, key >> 4, 64) * a.kv.heads + w.h) * rec + page * D;
+                st.ks = *reinterpret_cast<const u32x2_t *>(p + 2 * (b * page + ((k0 + key) & (page - 1))));
             }
         }
-        const uint8_t *vr = a.kv.v + record(g >> 1);
-        const int vslot = (int)(k0 + 8 * g) & (page - 1);
+        const int vslot = (k0 + 8 * g) & (page - 1);
 #pragma unroll
         for (int i = 0; i < NS; i++) {
             const int at = (d0 + 8 * i) * page + vslot;
@@ -165,11 +158,12 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                     st.vs[st.at(i)] = *reinterpret_cast<const half8 *>(
                         vr + page * D + 2 * (((wave * (D / 4) + 8 * i) >> 5) * page + vslot));
         }
+        pg = page_of(k0 + CH + 16 * (lane & 3));
     };
     // the tile to LDS; `plain`: every row sees all of it.  What no row sees has no
     // value, whatever the pool holds; infinities and NaN that only some rows see are
     // taken out (T.odd) and added by hand
-    auto store = [&](int64_t k0, bool plain) {
+    auto store = [&](int k0, bool plain) {
 #pragma unroll
         for (int i = 0; i < NS; i++) {
             const int e = lane + 64 * i, key = e / (D / 8), c = e - key * (D / 8);
@@ -220,7 +214,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
     };
 
     if (w.k0 < w.k1) load(w.k0);
-    for (int64_t k0 = w.k0; k0 < w.k1; k0 += CH) {
+    for (int k0 = w.k0; k0 < w.k1; k0 += CH) {
         const bool plain = k0 >= w.lo_all && k0 + CH <= w.hi_all && good == 15;  // uniform
         const int seen = good;
         if (tid == 0) T.odd = 0;
@@ -268,7 +262,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
 #pragma unroll
             for (int u = 0; u < 2; u++)
 #pragma unroll
-                for (int i = 0; i < 16; i++) s[u][i] = attn_score(s[u][i], mul, a.softcap);
+                for (int i = 0; i < 16; i++) s[u][i] = capped(s[u][i] * mul, a.softcap);
             mm = 1.f;
         }
         if (!plain) {
@@ -311,10 +305,11 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         for (int f = 0; f < 4; f++) {
             half8 ph, pl;
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const float p = s[f >> 1][8 * (f & 1) + i];
-                ph[i] = (_Float16)p;
-                pl[i] = (_Float16)fmaf((float)ph[i], -1.f, p);
+            for (int i = 0; i < 8; i += 2) {
+                half2_t h, r;
+                split2(s[f >> 1][8 * (f & 1) + i], s[f >> 1][8 * (f & 1) + i + 1], h, r);
+                ph[i] = h.x, ph[i + 1] = h.y;
+                pl[i] = r.x, pl[i + 1] = r.y;
             }
             half8 pd;
             if constexpr (Q8) pd = ph * (_Float16)0.0078125f;
@@ -331,12 +326,12 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         }
         if (!plain && T.odd) {  // rare: infinities or NaN that only some rows see
             for (int j = 0; j < CH; j++) {
-                const int64_t k = k0 + j;
+                const int k = k0 + j;
                 if (k >= w.lo_all && k < w.hi_all) continue;
-                const int pg = kv_page(a.kv, w.s, k);
-                if (pg < 0) continue;
-                const uint8_t *p = a.kv.v + ((int64_t)pg * a.kv.heads + w.h) * rec;
-                const int slot = (int)k & (page - 1);
+                const int pj = page_of(k);
+                if (pj < 0) continue;
+                const uint8_t *p = a.kv.v + ((int64_t)pj * a.kv.heads + w.h) * rec;
+                const int slot = k & (page - 1);
 #pragma unroll
                 for (int d = 0; d < ND; d++)
 #pragma unroll

@@ -145,17 +145,18 @@ def _moe(args):
 def _case(args):
     import torch
 
-    from perf import operators
-    cases = {c["name"]: c for c in operators.listed()}
+    from perf import more_operators, operators
+    cases = {c["name"]: (m, c) for m in (operators, more_operators) for c in m.listed()}
     if args.name not in cases:
         raise SystemExit(f"no case {args.name!r}; listed are {', '.join(cases)}")
-    operators.own = True
+    module, case = cases[args.name]
+    module.own = True
     states, held = [], 0
     while held < 1 << 30 and len(states) < 16:
-        states.append(operators.prepare(cases[args.name], len(states)))
+        states.append(module.prepare(case, len(states)))
         held += sum(v.nbytes for v in states[-1].values() if isinstance(v, torch.Tensor))
     for r in range(args.reps):
-        operators.run(states[r % len(states)])
+        module.run(states[r % len(states)])
     torch.cuda.synchronize()
     print(f"case {args.name} x {args.reps} ({len(states)} inputs, {held >> 20} MiB)", flush=True)
 

@@ -493,8 +493,8 @@ typedef struct qmm_kv_cache {
  * while they change.  What they may hold: a token without a page (an index
  * below 0 or at max_pages * page or more, or a page id outside 0 .. pages-1) is
  * no token: it is not stored, and attention does not see it.  1 <= seqs, max_new,
- * max_pages, rows; seqs * max_new, rows and max_pages * page at most 2^31 - 1, seqs at
- * most 65535; max_pages <= table_stride: else QMM_ERR_SHAPE.  A sequence with
+ * max_pages, rows; seqs * max_new and rows at most 2^31 - 1, max_pages * page at most 2^30, seqs
+ * at most 65535; max_pages <= table_stride: else QMM_ERR_SHAPE.  A sequence with
  * more than max_new rows in starts: its rows from max_new on are left alone.
  * The structs are read before a call returns and not kept. */
 typedef struct qmm_kv_batch {
