@@ -500,19 +500,42 @@ def qmm_moe_down(w, dtype: int, E: int, M: int, K: int, N: int, T: int, ids, wei
         raise QmmError(rc, "qmm_moe_down")
 
 
-def _rows(t, rows: int, width: int, stride: int, what: str) -> int:
+def _current_device() -> int:
+    import torch
+    raw = getattr(torch._C, "_cuda_getDevice", None)  # the index alone: torch.cuda.current_device costs four times as much
+    return raw() if raw is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _on(dev, t, need: int, what: str, dtype) -> int:
+    """Address of a contiguous tensor of at least `need` values on device `dev`,
+    the current one (the kernels run there); None: 0; an address as it is."""
+    if t is None:
+        return 0
+    if type(t) is int:
+        return t
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be a tensor of the current device cuda:{dev}, it is on {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.numel() < need:
+        raise ValueError(f"{what} holds {t.numel()} values, needs {need}")
+    return t.data_ptr()
+
+
+def _rows(dev, t, rows: int, width: int, stride: int, what: str, dtype) -> int:
     """Address of f32 rows of `width` values that lie `stride` values apart (0:
     side by side).  The tensor may be a view into wider rows (columns of a fused
     projection); what the rows reach must lie inside its storage."""
-    import torch
-    if t is None or isinstance(t, int):
-        return t or 0
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a device tensor")
-    if t.dtype is not torch.float32:
-        raise ValueError(f"{what} must be {torch.float32}, got {t.dtype}")
-    if not stride:
-        return _addr(t, 4 * rows * width, what, torch.float32)
+    if not stride or t is None or type(t) is int:
+        return _on(dev, t, rows * width, what, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be a tensor of the current device cuda:{dev}, it is on {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.dim() == 2 and t.stride() == (stride, 1) and t.shape[0] >= rows and t.shape[1] >= width:
+        return t.data_ptr()
     if t.dim() and (t.stride(-1) != 1 or (t.dim() > 1 and t.shape[0] > 1 and t.stride(0) != stride)):
         raise ValueError(f"{what} must have rows {stride} values apart")
     if rows > 0 and width > 0:
@@ -522,16 +545,13 @@ def _rows(t, rows: int, width: int, stride: int, what: str) -> int:
     return t.data_ptr()
 
 
-def _on_current_device(*tensors) -> None:
-    """The kernels run on the current device: tensors of another are refused."""
-    import torch
-    at = None
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and t.is_cuda:
-            if at is None:
-                at = torch.cuda.current_device()
-            if t.device.index != at:
-                raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{at}")
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(dev)
+    return _stream(stream)
 
 
 def kv_pool_bytes(dtype: int, pages: int, page: int, heads: int, dim: int) -> int:
@@ -560,6 +580,11 @@ class KvCache:
         self.dtype, self.pages, self.page, self.heads, self.dim = dtype, pages, page, heads, dim
         self.struct = _KvCacheStruct(_addr(k, need, "k"), _addr(v, need, "v"), pages, dtype, page, heads, dim)
         self.ref = ctypes.addressof(self.struct)
+        self.devices = {t.get_device() for t in (k, v) if not isinstance(t, int) and t is not None}
+
+    def _check(self, dev: int) -> None:
+        if any(d != dev for d in self.devices):
+            raise ValueError(f"the cache's pools must be tensors of the current device cuda:{dev}")
 
 
 class KvBatch:
@@ -578,15 +603,19 @@ class KvBatch:
                                      _addr(starts, 4 * (seqs + 1), "starts", i32), seqs, max_pages, table_stride, max_new,
                                      rows)
         self.ref = ctypes.addressof(self.struct)
+        self.devices = {t.get_device() for t in (table, lens, starts) if not isinstance(t, int) and t is not None}
+
+    def _check(self, dev: int) -> None:
+        if any(d != dev for d in self.devices):
+            raise ValueError(f"the batch's arrays must be tensors of the current device cuda:{dev}")
 
 
 def qmm_rope_freqs(rot: int, base: float, freqs, factor: float = 1.0, context: float = 0.0, beta_fast: float = 32.0,
                    beta_slow: float = 1.0, factors=None, stream=None) -> None:
     import torch
-    _on_current_device(freqs, factors)
-    rc = lib().qmm_rope_freqs(rot, base, factor, context, beta_fast, beta_slow,
-                              _addr(factors, 2 * rot, "factors", torch.float32),
-                              _addr(freqs, 2 * rot, "freqs", torch.float32), _stream(stream))
+    dev, f32 = _current_device(), torch.float32
+    rc = lib().qmm_rope_freqs(rot, base, factor, context, beta_fast, beta_slow, _on(dev, factors, rot // 2, "factors", f32),
+                              _on(dev, freqs, rot // 2, "freqs", f32), _raw_stream(stream, dev))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_rope_freqs")
 
@@ -594,10 +623,10 @@ def qmm_rope_freqs(rot: int, base: float, freqs, factor: float = 1.0, context: f
 def qmm_rope(X, N: int, H: int, D: int, pos, freqs, rot: int, Y, layout: int = QMM_ROPE_HALF, mscale: float = 1.0,
              x_stride: int = 0, y_stride: int = 0, stream=None) -> None:
     import torch
-    _on_current_device(X, pos, freqs, Y)
-    rc = lib().qmm_rope(_rows(X, N, H * D, x_stride, "X"), x_stride, N, H, D, _addr(pos, 4 * N, "pos", torch.int32),
-                        _addr(freqs, 2 * rot, "freqs", torch.float32), rot, layout, mscale,
-                        _rows(Y, N, H * D, y_stride, "Y"), y_stride, _stream(stream))
+    dev, f32 = _current_device(), torch.float32
+    rc = lib().qmm_rope(_rows(dev, X, N, H * D, x_stride, "X", f32), x_stride, N, H, D,
+                        _on(dev, pos, N, "pos", torch.int32), _on(dev, freqs, rot // 2, "freqs", f32), rot, layout, mscale,
+                        _rows(dev, Y, N, H * D, y_stride, "Y", f32), y_stride, _raw_stream(stream, dev))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_rope")
 
@@ -606,14 +635,16 @@ def qmm_kv_append(cache: KvCache, batch: KvBatch, K, V, freqs=None, rot: int = 0
                   mscale: float = 1.0, pos=None, k_norm=None, q_norm=None, eps: float = 1e-5, Q=None, q_heads: int = 0,
                   q_out=None, q_stride: int = 0, k_stride: int = 0, v_stride: int = 0, stream=None) -> None:
     import torch
-    f32, D, rows = torch.float32, cache.dim, batch.rows
-    _on_current_device(cache.k, cache.v, batch.table, batch.lens, batch.starts, K, V, freqs, pos, k_norm, q_norm, Q, q_out)
-    rc = lib().qmm_kv_append(cache.ref, batch.ref, _rows(K, rows, cache.heads * D, k_stride, "K"), k_stride,
-                             _rows(V, rows, cache.heads * D, v_stride, "V"), v_stride, _addr(freqs, 2 * rot, "freqs", f32),
-                             rot, layout, mscale, _addr(pos, 4 * rows, "pos", torch.int32),
-                             _addr(k_norm, 4 * D, "k_norm", f32), _addr(q_norm, 4 * D, "q_norm", f32), eps,
-                             _rows(Q, rows, q_heads * D, q_stride, "Q"), q_stride, q_heads,
-                             _addr(q_out, 4 * rows * q_heads * D, "q_out", f32), _stream(stream))
+    dev, f32, D, rows = _current_device(), torch.float32, cache.dim, batch.rows
+    cache._check(dev)
+    batch._check(dev)
+    wide = cache.heads * D
+    rc = lib().qmm_kv_append(cache.ref, batch.ref, _rows(dev, K, rows, wide, k_stride, "K", f32), k_stride,
+                             _rows(dev, V, rows, wide, v_stride, "V", f32), v_stride,
+                             _on(dev, freqs, rot // 2, "freqs", f32), rot, layout, mscale,
+                             _on(dev, pos, rows, "pos", torch.int32), _on(dev, k_norm, D, "k_norm", f32),
+                             _on(dev, q_norm, D, "q_norm", f32), eps, _rows(dev, Q, rows, q_heads * D, q_stride, "Q", f32),
+                             q_stride, q_heads, _on(dev, q_out, rows * q_heads * D, "q_out", f32), _raw_stream(stream, dev))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_kv_append")
 
@@ -627,10 +658,13 @@ def qmm_attention(cache: KvCache, batch: KvBatch, Q, q_heads: int, out, scale: f
                   window: int = 0, softcap: float = 0.0, work=None, q_stride: int = 0, stream=None) -> None:
     """scale None: 1 / sqrt(dim)."""
     import torch
-    D, rows = cache.dim, batch.rows
-    _on_current_device(cache.k, cache.v, batch.table, batch.lens, batch.starts, Q, out, work)
-    rc = lib().qmm_attention(cache.ref, batch.ref, _rows(Q, rows, q_heads * D, q_stride, "Q"), q_stride, q_heads,
+    dev, f32, D, rows = _current_device(), torch.float32, cache.dim, batch.rows
+    cache._check(dev)
+    batch._check(dev)
+    if work is not None and not isinstance(work, int) and work.get_device() != dev:
+        raise ValueError(f"work must be a tensor of the current device cuda:{dev}, it is on {work.device}")
+    rc = lib().qmm_attention(cache.ref, batch.ref, _rows(dev, Q, rows, q_heads * D, q_stride, "Q", f32), q_stride, q_heads,
                              D ** -0.5 if scale is None else scale, int(bool(causal)), window, softcap,
-                             _addr(out, 4 * rows * q_heads * D, "out", torch.float32), *_work(work), _stream(stream))
+                             _on(dev, out, rows * q_heads * D, "out", f32), *_work(work), _raw_stream(stream, dev))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_attention")

@@ -129,7 +129,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float attn_mul(const AttnArgs &a, int e) {
     return ldexpf(a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e, -e);
 }
-__device__ __forceinline__ float capped(float x, float softcap) { return softcap * kLog2e * tanhf(x); }
+// softcap * tanh(x) in base 2, within 2^-22 of softcap: tanh(x) = 1 - 2 / (e^2x + 1)
+__device__ __forceinline__ float capped(float x, float softcap) {
+    const float t = 1.f - 2.f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.f * kLog2e * x) + 1.f);
+    return softcap * kLog2e * t;
+}
 
 // p = hi + lo in f16 to 2^-23 of p (2^-25 near 0): two conversions for two values and one FMA
 // that reads its f16 operand as it is for each rest (p - hi, exact).  The rests

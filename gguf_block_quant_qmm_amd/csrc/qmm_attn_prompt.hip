@@ -53,7 +53,7 @@ template <int D, bool Q8> struct Tile {  // in LDS
     _Float16 k[CH][KP];
     _Float16 v[Q8 ? 2 : 1][D][VP];
     _Float16 ks[Q8 ? D / 32 : 1][CH];
-    int odd;
+    int odd[4];  // per wavefront
 };
 
 // Token t of a tile <-> row of the first product: bits 2 and 3 exchanged.
@@ -210,52 +210,66 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
             *reinterpret_cast<half8 *>(&T.v[0][d][8 * g]) = x;
             if constexpr (Q8) *reinterpret_cast<half8 *>(&T.v[1][d][8 * g]) = y;
         }
-        if (odd) T.odd = 1;
+        if (!plain && lane == 0) T.odd[wave] = 0;
+        if (odd) T.odd[wave] = 1;
     };
 
     if (w.k0 < w.k1) load(w.k0);
     for (int k0 = w.k0; k0 < w.k1; k0 += CH) {
         const bool plain = k0 >= w.lo_all && k0 + CH <= w.hi_all && good == 15;  // uniform
         const int seen = good;
-        if (tid == 0) T.odd = 0;
         __syncthreads();  // the last tile's reads are done
         store(k0, plain);
         __syncthreads();
         if (k0 + CH < w.k1) load(k0 + CH);
         if (!wave_on) continue;
+        // the products first: a wavefront in its softmax fills what they leave of the issue
+        __builtin_amdgcn_s_setprio(1);
         floatx16 s[2];
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
+        for (int u = 0; u < 2; u++)
 #pragma unroll
             for (int i = 0; i < 16; i++) s[u][i] = 0.f;
-            if constexpr (Q8) {
+        if constexpr (Q8) {
 #pragma unroll
-                for (int b = 0; b < D / 32; b++) {
-                    floatx16 z;
+            for (int b = 0; b < D / 32; b++) {
+                floatx16 z[2];
 #pragma unroll
-                    for (int i = 0; i < 16; i++) z[i] = 0.f;
+                for (int u = 0; u < 2; u++)
 #pragma unroll
-                    for (int f = 0; f < 2; f++) {
-                        const half8 kf = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][32 * b + 16 * f + 8 * hh]);
-                        z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[2 * b + f], z, 0, 0, 0);
-                        z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[2 * b + f], z, 0, 0, 0);
-                    }
+                    for (int i = 0; i < 16; i++) z[u][i] = 0.f;
+#pragma unroll
+                for (int f = 0; f < 2; f++) {
+                    half8 kf[2];
+#pragma unroll
+                    for (int u = 0; u < 2; u++) kf[u] = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][32 * b + 16 * f + 8 * hh]);
+#pragma unroll
+                    for (int u = 0; u < 2; u++) z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], ql[2 * b + f], z[u], 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < 2; u++) z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], qh[2 * b + f], z[u], 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; u++)
 #pragma unroll
                     for (int f = 0; f < 2; f++) {
                         const half8 sc = *reinterpret_cast<const half8 *>(&T.ks[b][32 * u + 16 * f + 8 * hh]);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) s[u][8 * f + i] = fmaf(z[8 * f + i], (float)sc[i], s[u][8 * f + i]);
+                        for (int i = 0; i < 8; i++) s[u][8 * f + i] = fmaf(z[u][8 * f + i], (float)sc[i], s[u][8 * f + i]);
                     }
-                }
-            } else {
+            }
+        } else {
 #pragma unroll
-                for (int b = 0; b < NK; b++) {
-                    const half8 kf = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][16 * b + 8 * hh]);
-                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[b], s[u], 0, 0, 0);
-                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[b], s[u], 0, 0, 0);
-                }
+            for (int b = 0; b < NK; b++) {
+                half8 kf[2];
+#pragma unroll
+                for (int u = 0; u < 2; u++) kf[u] = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][16 * b + 8 * hh]);
+#pragma unroll
+                for (int u = 0; u < 2; u++) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], ql[b], s[u], 0, 0, 0);
+#pragma unroll
+                for (int u = 0; u < 2; u++) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], qh[b], s[u], 0, 0, 0);
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         float mm = mul;
         if (a.softcap > 0.f) {  // uniform
@@ -301,6 +315,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                 l += s[u][i];
             }
         __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int f = 0; f < 4; f++) {
             half8 ph, pl;
@@ -324,7 +339,8 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                 }
             }
         }
-        if (!plain && T.odd) {  // rare: infinities or NaN that only some rows see
+        __builtin_amdgcn_s_setprio(0);
+        if (!plain && (T.odd[0] | T.odd[1] | T.odd[2] | T.odd[3])) {  // rare: infinities or NaN that only some rows see
             for (int j = 0; j < CH; j++) {
                 const int k = k0 + j;
                 if (k >= w.lo_all && k < w.hi_all) continue;
@@ -381,11 +397,13 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
 template <int D>
 hipError_t launch_d(AttnArgs a, int dtype, int64_t blocks, hipStream_t st) {
     constexpr int64_t kBlocks = int64_t(1) << 23;
+    constexpr size_t lds_q8 = sizeof(Tile<D, true>);
+    constexpr size_t lds_f16 = sizeof(Tile<D, false>);
     for (int64_t b = 0; b < blocks; b += kBlocks) {
         a.block0 = b;
         const dim3 grid((unsigned)(blocks - b < kBlocks ? blocks - b : kBlocks));
-        if (dtype == QMM_Q8_0) hipLaunchKernelGGL((attn_prompt_kernel<D, true>), grid, dim3(256), sizeof(Tile<D, true>), st, a);
-        else hipLaunchKernelGGL((attn_prompt_kernel<D, false>), grid, dim3(256), sizeof(Tile<D, false>), st, a);
+        if (dtype == QMM_Q8_0) hipLaunchKernelGGL((attn_prompt_kernel<D, true>), grid, dim3(256), lds_q8, st, a);
+        else hipLaunchKernelGGL((attn_prompt_kernel<D, false>), grid, dim3(256), lds_f16, st, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -15,8 +15,9 @@
 // while a wavefront works out the angles.
 //
 // The append's values go to pages with the token index inside, so a workgroup
-// takes a head's tile of TS neighbouring token places: rows in, through LDS,
-// places out, 16 bytes (8 places) a thread where all 8 are new.
+// takes TS neighbouring token places of 64 dims of a head: rows in, through LDS,
+// places out, 16 bytes (8 places) a thread where all 8 are new.  (17 KB of LDS: whole
+// heads of 128, 34 KB, halve the wavefronts of the turning workgroups in the same launch.)
 #include "qmm_internal.hpp"
 #include "qmm_kv.hpp"
 #include "qmm_units.hpp"
@@ -45,37 +46,49 @@ __device__ __forceinline__ int q8_code(float v, float id) {
     return (int)(q != q ? 0.0f : fminf(fmaxf(q, -128.0f), 127.0f));
 }
 
-// The values of one head in TS neighbouring places (index t0 .. t0 + TS - 1).
+// The values of 64 dims (or the last 32) of one head in TS neighbouring places (index
+// t0 .. t0 + TS - 1).
+constexpr int kDims = 64, kPitch = kDims + 1;
 template <int DT, int TS>
 __device__ __forceinline__ void put_values(const TurnArgs &a, int64_t vb, float *tile) {
     const KvArgs &kv = a.kv;
-    const int t = (int)threadIdx.x, D = a.D, pitch = D + 1;
+    const int t = (int)threadIdx.x, D = a.D, parts = (D + kDims - 1) / kDims;
+    const uint32_t heads = (uint32_t)(a.Hk * parts);
     int h, s, k;
-    if (a.v_tiles * kv.seqs * a.Hk <= UINT32_MAX) {  // uniform
+    if (a.v_tiles * kv.seqs * heads <= UINT32_MAX) {  // uniform
         const uint32_t b = (uint32_t)vb;
-        h = (int)(b % (uint32_t)a.Hk);
-        s = (int)(b / (uint32_t)a.Hk % (uint32_t)kv.seqs);
-        k = (int)(b / (uint32_t)a.Hk / (uint32_t)kv.seqs);
+        h = (int)(b % heads);
+        s = (int)(b / heads % (uint32_t)kv.seqs);
+        k = (int)(b / heads / (uint32_t)kv.seqs);
     } else {
-        h = (int)(vb % a.Hk);
-        s = (int)(vb / a.Hk % kv.seqs);
-        k = (int)(vb / a.Hk / kv.seqs);
+        h = (int)(vb % heads);
+        s = (int)(vb / heads % kv.seqs);
+        k = (int)(vb / heads / kv.seqs);
     }
+    const int first = h % parts * kDims, W = D - first < kDims ? D - first : kDims;
+    h /= parts;
     const KvNew nw = kv_new(kv, s);
     if (nw.count == 0 || nw.index + nw.count <= 0) return;
     const int64_t lo = nw.index > 0 ? nw.index : 0, hi = nw.index + nw.count;  // places lo .. hi - 1 are new
     const int64_t t0 = (lo / TS + k) * TS;
     if (t0 >= hi) return;
-    for (int e = t; e < TS * D; e += 256) {
-        const int j = e / D, d = e - j * D;
-        const int64_t i = t0 + j;
-        if (i >= lo && i < hi)
-            tile[j * pitch + d] = a.v[((int64_t)nw.first + (i - nw.index)) * a.v_stride + (int64_t)h * D + d];
+    const float *src = a.v + (int64_t)h * D + first;
+    float x[TS * kDims / 256];
+#pragma unroll
+    for (int i = 0; i < TS * kDims / 256; i++) {  // all loads under way at once
+        const int e = t + 256 * i, d = e % kDims;
+        const int64_t at = t0 + e / kDims;
+        x[i] = at >= lo && at < hi && d < W ? src[((int64_t)nw.first + (at - nw.index)) * a.v_stride + d] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < TS * kDims / 256; i++) {
+        const int e = t + 256 * i;
+        tile[e / kDims * kPitch + e % kDims] = x[i];
     }
     __syncthreads();
-    const int page = 1 << kv.page_shift, nb = D / 32;
+    const int page = 1 << kv.page_shift, nb = W / 32;
     const int64_t rec = kv_record(DT, page, D);
-    float *inv = tile + TS * pitch;  // Q8_0: 1/d of [block][place]
+    float *inv = tile + TS * kPitch;  // Q8_0: 1/d of [block][place]
     if constexpr (DT == QMM_Q8_0) {
         for (int e = t; e < TS * nb; e += 256) {
             const int j = e % TS, b = e / TS;
@@ -84,34 +97,34 @@ __device__ __forceinline__ void put_values(const TurnArgs &a, int64_t vb, float 
             float amax = 0.f, d, id;
 #pragma unroll 8
             for (int c = 0; c < 32; c++) {
-                const float x = fabsf(tile[j * pitch + 32 * b + c]);
-                amax = x > amax ? x : amax;  // a NaN never wins
+                const float y = fabsf(tile[j * kPitch + 32 * b + c]);
+                amax = y > amax ? y : amax;  // a NaN never wins
             }
             q8_scale(amax, d, id);
             inv[e] = id;
             const int pg = kv_page(kv, s, i);
             if (pg >= 0) {
                 _Float16 *sc = reinterpret_cast<_Float16 *>(kv.v + ((int64_t)pg * kv.heads + h) * rec + (int64_t)page * D);
-                sc[b * page + (int)(i & (page - 1))] = (_Float16)d;
+                sc[(first / 32 + b) * page + (int)(i & (page - 1))] = (_Float16)d;
             }
         }
         __syncthreads();
     }
-    for (int e = t; e < D * (TS / 8); e += 256) {
+    for (int e = t; e < W * (TS / 8); e += 256) {
         const int g = e % (TS / 8), d = e / (TS / 8);
         const int64_t i = t0 + 8 * g;
         if (i + 8 <= lo || i >= hi) continue;
         const int pg = kv_page(kv, s, i);  // 8 neighbours share a page
         if (pg < 0) continue;
         uint8_t *r = kv.v + ((int64_t)pg * kv.heads + h) * rec;
-        const int at = d * page + (int)(i & (page - 1));
+        const int at = (first + d) * page + (int)(i & (page - 1));
         const bool whole = i >= lo && i + 8 <= hi;
-        const float *src = tile + 8 * g * pitch + d;
+        const float *from = tile + 8 * g * kPitch + d;
         if constexpr (DT == QMM_F16) {
             _Float16 *o = reinterpret_cast<_Float16 *>(r) + at;
             half8 w;
 #pragma unroll
-            for (int j = 0; j < 8; j++) w[j] = (_Float16)src[j * pitch];
+            for (int j = 0; j < 8; j++) w[j] = (_Float16)from[j * kPitch];
             if (whole) {
                 *reinterpret_cast<half8 *>(o) = w;
             } else {
@@ -124,7 +137,7 @@ __device__ __forceinline__ void put_values(const TurnArgs &a, int64_t vb, float 
             uint32_t w[2] = {0u, 0u};
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                w[j / 4] |= ((uint32_t)q8_code(src[j * pitch], inv[(d / 32) * TS + 8 * g + j]) & 0xFFu) << (8 * (j % 4));
+                w[j / 4] |= ((uint32_t)q8_code(from[j * kPitch], inv[(d / 32) * TS + 8 * g + j]) & 0xFFu) << (8 * (j % 4));
             if (whole) {
                 *reinterpret_cast<u32x2_t *>(o) = u32x2_t{w[0], w[1]};
             } else {
@@ -300,7 +313,7 @@ constexpr int64_t kBlocks = int64_t(1) << 22;  // of a launch: fewer than 2^32 t
 
 template <int DT, int TS>
 hipError_t launch_turn(TurnArgs a, int64_t rows, unsigned threads, size_t lds, hipStream_t st) {
-    const int64_t v_blocks = DT ? a.v_tiles * a.kv.seqs * a.Hk : 0;
+    const int64_t v_blocks = DT ? a.v_tiles * a.kv.seqs * a.Hk * ((a.D + kDims - 1) / kDims) : 0;
     int64_t n = 0, v = 0;
     while (n < rows || v < v_blocks) {
         const int64_t take = rows - n < kBlocks / a.bpt ? rows - n : kBlocks / a.bpt;
@@ -377,18 +390,15 @@ hipError_t launch_kv_append(const qmm_kv_cache &cache, const qmm_kv_batch &batch
     a.bpt = (a.Hq + a.Hk + a.hpb - 1) / a.hpb;
     const size_t turn_lds = (size_t)a.rot / 2 * 16 + 256 * 8 + (cache.dtype == QMM_Q8_0 ? 256 * 8 * 4 : 0);
     auto lds = [&](int ts) {
-        const size_t tile = ((size_t)ts * (a.D + 1) + (size_t)ts * (a.D / 32)) * 4;
+        const size_t tile = ((size_t)ts * kPitch + (size_t)ts * (kDims / 32)) * 4;
         return tile > turn_lds ? tile : turn_lds;
     };
-    // tiles of 16 places for few new tokens, else 64 (a 128-byte line of f16 places); 32 where 64 are
-    // over 64 KB of LDS
-    const int ts = batch.max_new < 32 ? 16 : a.D <= 192 ? 64 : 32;
+    // tiles of 16 places for few new tokens, else 64 (a 128-byte line of f16 places)
+    const int ts = batch.max_new < 32 ? 16 : 64;
     a.v_tiles = (batch.max_new + 2 * ts - 2) / ts;
     const int64_t rows = batch.rows;
-#define QMM_TURN(DT)                                              \
-    (ts == 16   ? launch_turn<DT, 16>(a, rows, 256, lds(16), st) \
-     : ts == 32 ? launch_turn<DT, 32>(a, rows, 256, lds(32), st) \
-                : launch_turn<DT, 64>(a, rows, 256, lds(64), st))
+#define QMM_TURN(DT) \
+    (ts == 16 ? launch_turn<DT, 16>(a, rows, 256, lds(16), st) : launch_turn<DT, 64>(a, rows, 256, lds(64), st))
     return cache.dtype == QMM_F16 ? QMM_TURN(QMM_F16) : QMM_TURN(QMM_Q8_0);
 #undef QMM_TURN
 }
