@@ -105,7 +105,7 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, const Where &w, i
 // MODE 0: up to 8 rows a workgroup, both parts in one column tile; 1, 2: one or
 // two tiles of 16 rows, each part its own product.
 template <int D, bool Q8, int MODE>
-__global__ void __launch_bounds__(64 * kWaves, MODE == 0 && D <= 128 ? 3 : D <= 128 ? 2 : 1) attn_few_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : MODE == 0 ? 3 : 2) attn_few_kernel(const AttnArgs a) {
     constexpr int NC = MODE == 0 ? 1 : MODE, RT = MODE == 0 ? 8 : 16 * MODE, NK = D / 32, ND = D / 16;
     constexpr bool STACK = MODE == 0;
     __shared__ __attribute__((aligned(16))) float lo_[kWaves][16][D + 4];
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(64 * kWaves, MODE == 0 && D <= 128 ? 3 : D <= 
         for (int c = 0; c < NC; c++) mul[c] = lmul[c][col];
     }
 
+    const float m1 = opaque_minus_one();
     floatx4 o[NC][ND];
     float m[NC], l[NC];
     int top[NC];  // Q8_0: biased exponent of the largest value scale
@@ -383,8 +384,8 @@ __global__ void __launch_bounds__(64 * kWaves, MODE == 0 && D <= 128 ? 3 : D <= 
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     half2_t h, r;
-                    if constexpr (Q8) split2(s[c][j] * (float)x.vs[b][j], s[c][j + 1] * (float)x.vs[b][j + 1], h, r);
-                    else split2(s[c][j], s[c][j + 1], h, r);
+                    if constexpr (Q8) split2(s[c][j] * (float)x.vs[b][j], s[c][j + 1] * (float)x.vs[b][j + 1], m1, h, r);
+                    else split2(s[c][j], s[c][j + 1], m1, h, r);
                     if (STACK) h = col >= 8 ? r : h;
                     ph[c][j] = h.x, ph[c][j + 1] = h.y;
                     pl[c][j] = r.x, pl[c][j + 1] = r.y;

@@ -136,15 +136,17 @@ __device__ __forceinline__ float capped(float x, float softcap) {
 }
 
 // p = hi + lo in f16 to 2^-23 of p (2^-25 near 0): two conversions for two values and one FMA
-// that reads its f16 operand as it is for each rest (p - hi, exact).  The rests
-// come after the conversions of the same values, so no wait of a value's own producer is
-// left to them.
-__device__ __forceinline__ void split2(float p0, float p1, half2_t &hi, half2_t &lo) {
+// that reads its f16 operand as it is for each rest (p - hi, exact).  minus_one is
+// -1 where the compiler cannot see it: it would convert and subtract instead.
+__device__ __forceinline__ float opaque_minus_one() {
+    float v = -1.f;
+    asm("" : "+s"(v));
+    return v;
+}
+__device__ __forceinline__ void split2(float p0, float p1, float minus_one, half2_t &hi, half2_t &lo) {
     typedef float float2_t __attribute__((ext_vector_type(2)));
     hi = __builtin_convertvector((float2_t{p0, p1}), half2_t);
-    float r0, r1;
-    asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r0) : "v"(hi), "v"(p0));
-    asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r1) : "v"(hi), "v"(p1));
+    const float r0 = fmaf((float)hi.x, minus_one, p0), r1 = fmaf((float)hi.y, minus_one, p1);
     lo = __builtin_convertvector((float2_t{r0, r1}), half2_t);
 }
 

@@ -31,6 +31,7 @@ namespace qmm {
 namespace {
 
 constexpr int CH = kPromptChunk, RT = kPromptRows;
+constexpr int AHEAD = 2;  // steps that a read from LDS is ahead of its products (3: 8 % slower, the registers spill)
 
 // One tile on its way from memory to LDS.  Wavefront w brings the keys of the
 // tile's w-th run of 16 tokens (neighbours in their page: one piece of memory, from a
@@ -54,6 +55,10 @@ template <int D, bool Q8> struct Tile {  // in LDS
     _Float16 v[Q8 ? 2 : 1][D][VP];
     _Float16 ks[Q8 ? D / 32 : 1][CH];
     int odd[4];  // per wavefront
+    // the queries' second parts, a wavefront's own, where the registers cannot hold them and
+    // this does (16 query heads of 256, 512 tokens over 4096: 131 us, 160 with 133 registers spilled)
+    static constexpr bool QL = !Q8 && D == 256;
+    half8 ql[QL ? 4 : 1][QL ? D / 16 : 1][QL ? 64 : 1];
 };
 
 // Token t of a tile <-> row of the first product: bits 2 and 3 exchanged.
@@ -80,7 +85,8 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
     attn_sees(a, w.nw, t, lo, hi);
     if (!on) lo = hi = 0;
 
-    half8 qh[NK], ql[NK];
+    constexpr bool QL = Tile<D, Q8>::QL;
+    half8 qh[NK], ql[QL ? 1 : NK];
     float mul;
     {
         const float *q = a.Q + (int64_t)(w.nw.first + t) * a.q_stride + (int64_t)hq * D + 8 * hh;
@@ -104,14 +110,18 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         const bool neg = mul < 0.f;
         mul = fmaxf(fabsf(mul), 0x1p-126f);  // above 0: a masked -inf stays one
 #pragma unroll
-        for (int b = 0; b < NK; b++)
+        for (int b = 0; b < NK; b++) {
+            half8 rest;
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const float s = x[b][i / 4][i % 4], v = ldexpf(neg ? -s : s, e);
                 const _Float16 p = (_Float16)v;
                 qh[b][i] = p;
-                ql[b][i] = (_Float16)(v - (float)p);
+                rest[i] = (_Float16)(v - (float)p);
             }
+            if constexpr (QL) T.ql[wave][b][lane] = rest;
+            else ql[b] = rest;
+        }
     }
     floatx16 o[ND];
 #pragma unroll
@@ -119,6 +129,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
 #pragma unroll
         for (int i = 0; i < 16; i++) o[d][i] = 0.f;
     float base = -INFINITY, l = 0.f;
+    const float m1 = opaque_minus_one();
 
     Stage<D, Q8> st;
     int good = 0;  // which of the tile's four runs of 16 tokens have a page
@@ -223,81 +234,80 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         __syncthreads();
         if (k0 + CH < w.k1) load(k0 + CH);
         if (!wave_on) continue;
-        // the products first: a wavefront in its softmax fills what they leave of the issue
-        __builtin_amdgcn_s_setprio(1);
-        floatx16 s[2];
+        // Two halves of 32 tokens: while the matrix cores have one half's scores or outputs, the
+        // vector ALU has the other's softmax.  The products have priority, so that another
+        // wavefront's softmax fills what they leave of the issue.
+        const float mm = a.softcap > 0.f ? 1.f : mul;
+        const int from = within(lo - k0) - 8 * hh, end = within(hi - k0) - 8 * hh;
+        // One step is two products (three: Q8_0's outputs), the read for the step after the next and
+        // the part of a softmax that fits under them, in this order (the scheduler gathers the
+        // products at one end otherwise).
+        auto scores = [&](int u, floatx16 &s, auto under) {
+            half8 kf[AHEAD + 1], qr[QL ? AHEAD + 1 : 1];
+            auto read = [&](int i) { return *reinterpret_cast<const half8 *>(&T.k[32 * u + col][16 * i + 8 * hh]); };
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+            for (int i = 0; i < AHEAD; i++) {
+                kf[i] = read(i);
+                if constexpr (QL) qr[i] = T.ql[wave][i][lane];
+            }
 #pragma unroll
-            for (int i = 0; i < 16; i++) s[u][i] = 0.f;
-        if constexpr (Q8) {
+            for (int i = 0; i < 16; i++) s[i] = 0.f;
+            floatx16 z;
+            half8 sc[2];
 #pragma unroll
-            for (int b = 0; b < D / 32; b++) {
-                floatx16 z[2];
-#pragma unroll
-                for (int u = 0; u < 2; u++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) z[u][i] = 0.f;
-#pragma unroll
-                for (int f = 0; f < 2; f++) {
-                    half8 kf[2];
-#pragma unroll
-                    for (int u = 0; u < 2; u++) kf[u] = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][32 * b + 16 * f + 8 * hh]);
-#pragma unroll
-                    for (int u = 0; u < 2; u++) z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], ql[2 * b + f], z[u], 0, 0, 0);
-#pragma unroll
-                    for (int u = 0; u < 2; u++) z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], qh[2 * b + f], z[u], 0, 0, 0);
+            for (int i = 0; i < NK; i++) {
+                if (i + AHEAD < NK) {
+                    kf[(i + AHEAD) % (AHEAD + 1)] = read(i + AHEAD);
+                    if constexpr (QL) qr[(i + AHEAD) % (AHEAD + 1)] = T.ql[wave][i + AHEAD][lane];
                 }
+                half8 qlo;
+                if constexpr (QL) qlo = qr[i % (AHEAD + 1)];
+                else qlo = ql[i];
+                if constexpr (Q8) {
+                    if ((i & 1) == 0) {  // the first half of a block
 #pragma unroll
-                for (int u = 0; u < 2; u++)
+                        for (int f = 0; f < 2; f++) sc[f] = *reinterpret_cast<const half8 *>(&T.ks[i / 2][32 * u + 16 * f + 8 * hh]);
 #pragma unroll
-                    for (int f = 0; f < 2; f++) {
-                        const half8 sc = *reinterpret_cast<const half8 *>(&T.ks[b][32 * u + 16 * f + 8 * hh]);
-#pragma unroll
-                        for (int i = 0; i < 8; i++) s[u][8 * f + i] = fmaf(z[u][8 * f + i], (float)sc[i], s[u][8 * f + i]);
+                        for (int j = 0; j < 16; j++) z[j] = 0.f;
                     }
+                    z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[i % (AHEAD + 1)], qlo, z, 0, 0, 0);
+                    z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[i % (AHEAD + 1)], qh[i], z, 0, 0, 0);
+                    under(i);
+                    if (i & 1) {
+#pragma unroll
+                        for (int j = 0; j < 16; j++) s[j] = fmaf(z[j], (float)sc[j >> 3][j & 7], s[j]);
+                    }
+                } else {
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[i % (AHEAD + 1)], qlo, s, 0, 0, 0);
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[i % (AHEAD + 1)], qh[i], s, 0, 0, 0);
+                    under(i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-        } else {
+        };
+        // softcap and mask; true if the reference has to move to `mx`
+        float mx;
+        auto largest = [&](int u, floatx16 &s) {
+            if (a.softcap > 0.f) {  // uniform
 #pragma unroll
-            for (int b = 0; b < NK; b++) {
-                half8 kf[2];
-#pragma unroll
-                for (int u = 0; u < 2; u++) kf[u] = *reinterpret_cast<const half8 *>(&T.k[32 * u + col][16 * b + 8 * hh]);
-#pragma unroll
-                for (int u = 0; u < 2; u++) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], ql[b], s[u], 0, 0, 0);
-#pragma unroll
-                for (int u = 0; u < 2; u++) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[u], qh[b], s[u], 0, 0, 0);
+                for (int i = 0; i < 16; i++) s[i] = capped(s[i] * mul, a.softcap);
             }
-        }
-        __builtin_amdgcn_s_setprio(0);
-        __builtin_amdgcn_sched_barrier(0);
-        float mm = mul;
-        if (a.softcap > 0.f) {  // uniform
-#pragma unroll
-            for (int u = 0; u < 2; u++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) s[u][i] = capped(s[u][i] * mul, a.softcap);
-            mm = 1.f;
-        }
-        if (!plain) {
-            // register i of half hh is token 16 (i / 8) + 8 hh + i % 8 of its 32
-            const int from = within(lo - k0) - 8 * hh, end = within(hi - k0) - 8 * hh;
-#pragma unroll
-            for (int u = 0; u < 2; u++)
+            if (!plain) {
+                // register i of half hh is token 16 (i / 8) + 8 hh + i % 8 of its 32
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     const int j = 32 * u + 16 * (i >> 3) + (i & 7);
-                    if (!(seen >> (2 * u + (i >> 3)) & 1) || j < from || j >= end) s[u][i] = -INFINITY;
+                    if (!(seen >> (2 * u + (i >> 3)) & 1) || j < from || j >= end) s[i] = -INFINITY;
                 }
-        }
-        float mx = s[0][0];
+            }
+            mx = s[0];
 #pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) mx = fmaxf(mx, s[u][i]);
-        mx = fold32(mx, MaxOp()) * mm;
-        if (__ballot(mx > base + 15.f)) {
-            const float to = mx > base ? mx - 7.f : base;
+            for (int i = 1; i < 16; i++) mx = fmaxf(mx, s[i]);
+            mx = fold32(mx, MaxOp()) * mm;
+            return __ballot(mx > base + 15.f) != 0;
+        };
+        auto rescale = [&]() {
+            const float to = mx > base + 15.f ? mx - 7.f : base;  // rows that need not move stay, bit for bit
             const float alpha = base == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - to);
             base = to;
             l *= alpha;
@@ -305,40 +315,73 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
             for (int d = 0; d < ND; d++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) o[d][i] *= alpha;
-        }
-        const float sub = base == -INFINITY ? 0.f : -base;
+        };
+        // the share of step i (of NK) in the softmax of s
+        auto softmax = [&](int i, floatx16 &s, half8 (&ph)[2], half8 (&pl)[2]) {
+            const float sub = base == -INFINITY ? 0.f : -base;
 #pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], mm, sub));
-                l += s[u][i];
-            }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int f = 0; f < 4; f++) {
-            half8 ph, pl;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
+            for (int j = 2 * (8 * i / NK); j < 2 * (8 * (i + 1) / NK); j += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[j], mm, sub)), p1 = __builtin_amdgcn_exp2f(fmaf(s[j + 1], mm, sub));
+                l += p0 + p1;
                 half2_t h, r;
-                split2(s[f >> 1][8 * (f & 1) + i], s[f >> 1][8 * (f & 1) + i + 1], h, r);
-                ph[i] = h.x, ph[i + 1] = h.y;
-                pl[i] = r.x, pl[i + 1] = r.y;
+                split2(p0, p1, m1, h, r);
+                ph[j >> 3][j & 7] = h.x, ph[j >> 3][(j & 7) + 1] = h.y;
+                pl[j >> 3][j & 7] = r.x, pl[j >> 3][(j & 7) + 1] = r.y;
+            }
+        };
+        auto outputs = [&](int u, const half8 (&ph)[2], const half8 (&pl)[2], auto under) {
+            half8 vf[AHEAD + 1], vl[Q8 ? AHEAD + 1 : 1];
+            auto read = [&](int plane, int i) {
+                return *reinterpret_cast<const half8 *>(&T.v[plane][32 * (i % ND) + col][32 * u + 16 * (i / ND) + 8 * hh]);
+            };
+#pragma unroll
+            for (int i = 0; i < AHEAD; i++) {
+                vf[i] = read(0, i);
+                if constexpr (Q8) vl[i] = read(1, i);
             }
             half8 pd;
-            if constexpr (Q8) pd = ph * (_Float16)0.0078125f;
 #pragma unroll
-            for (int d = 0; d < ND; d++) {
-                const half8 vf = *reinterpret_cast<const half8 *>(&T.v[0][32 * d + col][16 * f + 8 * hh]);
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pl, o[d], 0, 0, 0);
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, ph, o[d], 0, 0, 0);
-                if constexpr (Q8) {
-                    const half8 vl = *reinterpret_cast<const half8 *>(&T.v[1][32 * d + col][16 * f + 8 * hh]);
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl, pd, o[d], 0, 0, 0);
+            for (int i = 0; i < NK; i++) {
+                const int f = i / ND, d = i % ND;
+                if (i + AHEAD < NK) {
+                    vf[(i + AHEAD) % (AHEAD + 1)] = read(0, i + AHEAD);
+                    if constexpr (Q8) vl[(i + AHEAD) % (AHEAD + 1)] = read(1, i + AHEAD);
                 }
+                if constexpr (Q8) {
+                    if (d == 0) pd = ph[f] * (_Float16)0.0078125f;
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[i % (AHEAD + 1)], pd, o[d], 0, 0, 0);
+                }
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[i % (AHEAD + 1)], pl[f], o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[i % (AHEAD + 1)], ph[f], o[d], 0, 0, 0);
+                under(i);
+                __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        auto nothing = [](int) {};
+        floatx16 s0, s1;
+        half8 p0h[2], p0l[2], p1h[2], p1l[2];
+        __builtin_amdgcn_s_setprio(1);
+        scores(0, s0, nothing);
+        __builtin_amdgcn_s_setprio(0);
+        if (largest(0, s0)) rescale();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+        scores(1, s1, [&](int i) { softmax(i, s0, p0h, p0l); });
+        // made above, not where they are used
+        asm volatile("" : "+v"(p0h[0]), "+v"(p0h[1]), "+v"(p0l[0]), "+v"(p0l[1]), "+v"(l));
+        __builtin_amdgcn_s_setprio(0);
+        if (largest(1, s1)) {  // the first half's outputs go in under the reference they have
+            outputs(0, p0h, p0l, nothing);
+#pragma unroll
+            for (int f = 0; f < 2; f++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) p0h[f][i] = p0l[f][i] = (_Float16)0.f;
+            rescale();
         }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+        outputs(0, p0h, p0l, [&](int i) { softmax(i, s1, p1h, p1l); });
+        outputs(1, p1h, p1l, nothing);
         __builtin_amdgcn_s_setprio(0);
         if (!plain && (T.odd[0] | T.odd[1] | T.odd[2] | T.odd[3])) {  // rare: infinities or NaN that only some rows see
             for (int j = 0; j < CH; j++) {
