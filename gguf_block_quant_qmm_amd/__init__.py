@@ -575,7 +575,9 @@ class KvCache:
     (any tensor type), described for the calls that take it (qmm_kv_cache)."""
 
     def __init__(self, k, v, dtype: int, pages: int, page: int, heads: int, dim: int):
-        need = kv_pool_bytes(dtype, pages, page, heads, dim) or None
+        need = kv_pool_bytes(dtype, pages, page, heads, dim)
+        if not need:  # before the struct's 32-bit fields cut a size down to a valid one
+            raise QmmError(QMM_ERR_SHAPE if dtype in (QMM_F16, QMM_Q8_0) else QMM_ERR_DTYPE, "KvCache")
         self.k, self.v = k, v
         self.dtype, self.pages, self.page, self.heads, self.dim = dtype, pages, page, heads, dim
         self.struct = _KvCacheStruct(_addr(k, need, "k"), _addr(v, need, "v"), pages, dtype, page, heads, dim)
@@ -596,6 +598,9 @@ class KvBatch:
                  table_stride: int = 0):
         import torch
         i32 = torch.int32
+        for v in (seqs, max_pages, max_new, rows, table_stride):
+            if not 0 <= v < 1 << 62:  # a 64-bit field would cut it
+                raise QmmError(QMM_ERR_SHAPE, "KvBatch")
         self.table, self.lens, self.starts = table, lens, starts
         self.seqs, self.max_pages, self.max_new, self.rows = seqs, max_pages, max_new, rows
         wide = (seqs - 1) * (table_stride or max_pages) + max_pages
@@ -635,10 +640,11 @@ def qmm_kv_append(cache: KvCache, batch: KvBatch, K, V, freqs=None, rot: int = 0
                   mscale: float = 1.0, pos=None, k_norm=None, q_norm=None, eps: float = 1e-5, Q=None, q_heads: int = 0,
                   q_out=None, q_stride: int = 0, k_stride: int = 0, v_stride: int = 0, stream=None) -> None:
     import torch
-    dev, f32, D, rows = _current_device(), torch.float32, cache.dim, batch.rows
+    dev, f32 = _current_device(), torch.float32
+    D, rows = cache.struct.dim, batch.struct.rows  # what the call will use
     cache._check(dev)
     batch._check(dev)
-    wide = cache.heads * D
+    wide = cache.struct.heads * D
     rc = lib().qmm_kv_append(cache.ref, batch.ref, _rows(dev, K, rows, wide, k_stride, "K", f32), k_stride,
                              _rows(dev, V, rows, wide, v_stride, "V", f32), v_stride,
                              _on(dev, freqs, rot // 2, "freqs", f32), rot, layout, mscale,
@@ -658,7 +664,8 @@ def qmm_attention(cache: KvCache, batch: KvBatch, Q, q_heads: int, out, scale: f
                   window: int = 0, softcap: float = 0.0, work=None, q_stride: int = 0, stream=None) -> None:
     """scale None: 1 / sqrt(dim)."""
     import torch
-    dev, f32, D, rows = _current_device(), torch.float32, cache.dim, batch.rows
+    dev, f32 = _current_device(), torch.float32
+    D, rows = cache.struct.dim, batch.struct.rows  # what the call will use
     cache._check(dev)
     batch._check(dev)
     if work is not None and not isinstance(work, int) and work.get_device() != dev:

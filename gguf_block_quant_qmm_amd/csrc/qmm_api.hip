@@ -204,6 +204,7 @@ int check_attention(const qmm_kv_cache *c, const qmm_kv_batch *b, int64_t q_head
     if (q_heads < c->heads || q_heads > 65536 || q_heads % c->heads != 0) return QMM_ERR_SHAPE;
     // a sequence's query rows of one key-value head are counted in 31 bits, as are the units
     if (b->max_new > INT32_MAX / (q_heads / c->heads) || b->seqs * c->heads > INT32_MAX) return QMM_ERR_SHAPE;
+    if (b->rows > (int64_t(1) << 40) / q_heads) return QMM_ERR_SHAPE;  // the work bytes stay below 2^63
     return QMM_OK;
 }
 
@@ -229,7 +230,7 @@ const char *qmm_strerror(int code) {
     switch (code) {
     case QMM_OK: return "ok";
     case QMM_ERR_NULL: return "a required pointer is NULL";
-    case QMM_ERR_DTYPE: return "unsupported dtype (expected Q4_0=2, Q4_1=3, Q8_0=8, Q4_K=12, Q5_K=13 or Q6_K=14)";
+    case QMM_ERR_DTYPE: return "unsupported dtype (weights: Q4_0=2, Q4_1=3, Q8_0=8, Q4_K=12, Q5_K=13 or Q6_K=14; caches: F16=1 or Q8_0=8)";
     case QMM_ERR_SHAPE: return "bad shape (need M >= 1, N >= 1, K a positive multiple of the block size)";
     case QMM_ERR_ALIGN: return "misaligned pointer (blob and x/X need 16-byte, y/Y 4-byte alignment)";
     case QMM_ERR_DEVICE: return "no current HIP device, or it is not gfx950";

@@ -571,7 +571,7 @@ struct Plan {
 Plan plan_of(const qmm_kv_cache &c, const qmm_kv_batch &b, int64_t q_heads) {
     const int64_t G = q_heads / c.heads, rows = b.max_new * G, units = b.seqs * c.heads;
     Plan p;
-    p.mode = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
+    p.mode = rows >= tuning_lever("QMM_ATTN_PROMPT_FROM", 33) ? 3 : rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
     const int64_t rt = p.mode == 0 ? 8 : p.mode == 3 ? kPromptRows : 16 * p.mode;
     p.tiles = (int)((rows + rt - 1) / rt);
     const int64_t groups = units * p.tiles, tokens = b.max_pages * c.page;

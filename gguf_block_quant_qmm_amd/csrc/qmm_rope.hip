@@ -394,7 +394,7 @@ hipError_t launch_kv_append(const qmm_kv_cache &cache, const qmm_kv_batch &batch
         return tile > turn_lds ? tile : turn_lds;
     };
     // tiles of 16 places for few new tokens, else 64 (a 128-byte line of f16 places)
-    const int ts = batch.max_new < 32 ? 16 : 64;
+    const int ts = batch.max_new < tuning_lever("QMM_APPEND_TILE_FROM", 32) ? 16 : 64;
     a.v_tiles = (batch.max_new + 2 * ts - 2) / ts;
     const int64_t rows = batch.rows;
 #define QMM_TURN(DT) \

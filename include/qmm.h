@@ -591,7 +591,9 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
  * random data come within 1e-6 or so of the output's size.
  *   Q       device f32, row n's q_heads heads of dim values at Q + n * q_stride
  *           (0: q_heads * dim; a multiple of 4), 16-B aligned
- *   q_heads a multiple of cache->heads, at most 2^16, else QMM_ERR_SHAPE
+ *   q_heads a multiple of cache->heads, at most 2^16; rows * q_heads at most 2^40,
+ *           max_new * q_heads / heads and seqs * heads at most 2^31 - 1: else
+ *           QMM_ERR_SHAPE
  *   scale   finite; softcap finite, >= 0; window >= 0, and 0 unless causal: else
  *           QMM_ERR_VALUE
  *   out     device f32 [rows][q_heads * dim], 16-B aligned; rows of sequences
@@ -602,7 +604,8 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
  *           (two streams, two captured graphs) need separate work.
  * A row's result does not depend on the other sequences of the call, as long as
  * the sizes of cache, batch and q_heads are the same (they choose the form and
- * how the tokens are shared out).  Results are bitwise reproducible. */
+ * how the tokens are shared out: decoded tokens and prompts are faster in calls of
+ * their own, with a max_new and a max_pages that fit them).  Results are bitwise reproducible. */
 int64_t qmm_attention_work_bytes(const qmm_kv_cache *cache, const qmm_kv_batch *batch, int64_t q_heads);
 int qmm_attention(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const float *Q, int64_t q_stride, int64_t q_heads,
                   double scale, int causal, int64_t window, double softcap, float *out, void *work, int64_t work_bytes,

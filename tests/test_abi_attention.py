@@ -108,6 +108,7 @@ def attention(Q=A, q_stride=0, q_heads=8, scale=0.1, causal=1, window=0, softcap
     (dict(q_heads=0), q.QMM_ERR_SHAPE), (dict(q_heads=2), q.QMM_ERR_SHAPE), (dict(q_heads=10), q.QMM_ERR_SHAPE),
     (dict(q_heads=65540), q.QMM_ERR_SHAPE), (dict(q_stride=1020), q.QMM_ERR_SHAPE), (dict(q_stride=1026), q.QMM_ERR_SHAPE),
     (dict(heads=1, q_heads=64, seqs=1, max_new=1 << 26, rows=1 << 26), q.QMM_ERR_SHAPE),
+    (dict(rows=(1 << 31) - 1, starts=A, q_heads=1024), q.QMM_ERR_SHAPE),
     (dict(scale=math.nan), q.QMM_ERR_VALUE), (dict(scale=1e300), q.QMM_ERR_VALUE), (dict(softcap=-1.0), q.QMM_ERR_VALUE),
     (dict(softcap=math.inf), q.QMM_ERR_VALUE), (dict(window=-1), q.QMM_ERR_VALUE),
     (dict(window=5, causal=0), q.QMM_ERR_VALUE), (dict(Q=0), q.QMM_ERR_NULL), (dict(out=0), q.QMM_ERR_NULL),
@@ -146,3 +147,28 @@ def test_valid_calls_without_gpu_report_device():
     assert rope() == q.QMM_ERR_DEVICE and freqs() == q.QMM_ERR_DEVICE and append() == q.QMM_ERR_DEVICE
     assert attention() == q.QMM_ERR_DEVICE and attention(causal=0, starts=A, rows=1, dtype=8) == q.QMM_ERR_DEVICE
     assert append(Q=0, q_out=0, q_heads=0, freqs=0, rot=0, layout=9, dtype=8, starts=A, rows=1) == q.QMM_ERR_DEVICE
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(page=(1 << 32) + 64), q.QMM_ERR_SHAPE), (dict(heads=(1 << 32) + 4), q.QMM_ERR_SHAPE),
+    (dict(dim=(1 << 32) + 128), q.QMM_ERR_SHAPE), (dict(pages=0), q.QMM_ERR_SHAPE), (dict(dtype=2), q.QMM_ERR_DTYPE),
+])
+def test_cache_description_refuses_what_its_fields_would_cut(kw, code):
+    with pytest.raises(q.QmmError) as e:
+        q.KvCache(A, A, **{**dict(dtype=1, pages=10, page=64, heads=4, dim=128), **kw})
+    assert e.value.code == code
+
+
+@pytest.mark.parametrize("kw", [dict(seqs=-1), dict(rows=1 << 64), dict(max_pages=1 << 63), dict(max_new=-2)])
+def test_batch_description_refuses_what_its_fields_would_cut(kw):
+    with pytest.raises(q.QmmError) as e:
+        q.KvBatch(A, A, **{**dict(seqs=3, max_pages=8, max_new=2, rows=6), **kw})
+    assert e.value.code == q.QMM_ERR_SHAPE
+
+
+def test_host_tensors_are_refused():
+    import torch
+    with pytest.raises(ValueError, match="device"):
+        q.KvCache(torch.zeros(q.kv_pool_bytes(1, 2, 16, 1, 64), dtype=torch.uint8), A, 1, 2, 16, 1, 64)
+    with pytest.raises(ValueError, match="device"):
+        q.KvBatch(torch.zeros(4, dtype=torch.int32), A, 1, 4, 1, 1)
