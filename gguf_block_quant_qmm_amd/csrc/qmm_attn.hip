@@ -6,7 +6,10 @@
 // (x in base 2, m its running maximum), one pass over the row's tokens.
 //
 // Bound by memory: every key and value is read once for all G query heads of its
-// head and all new tokens.  The matrix cores do the products, because a row of f32
+// head and all new tokens (32/8 heads of 128, f16: one token over 131072 97 us and 5 for the join,
+// 5.6 TB/s; 64 sequences of 1 to 8192 225 + 7 us, 5.4 TB/s); few rounds of a
+// wavefront by latency (28 rows on a Q8_0 cache, 8 x 7 tokens to 4096: 35 + 5 us, a third of it the vector
+// ALU's; 513 tokens: 8.7 + 3.9).  The matrix cores do the products, because a row of f32
 // FMAs would cost as many instructions per query head as there are bytes:
 //   scores^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens' keys (a lane's 8
 //                      values are 16 bytes of its token's key), B = 16 columns of
@@ -561,7 +564,20 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
         if (64 * v + lane < D) a.out[rh * D + 64 * v + lane] = y[v] * inv;
 }
 
-// How a call is shared out: rows of a tile, row tiles of a sequence and head, splits of the tokens.
+// How a call is shared out: rows of a tile, row tiles of a sequence and head, splits of the tokens;
+// by sizes that the host knows, so that a captured call keeps it.  Measured with 32 query and 8
+// key-value heads of 128 (f16 unless said otherwise; a captured graph over inputs that rotate):
+//   form    rows of a key-value head (new tokens x G): up to 16 in one tile of 16 26.5 us (the form
+//           for many rows 31.8), 32 in two 30.0 (33.3), Q8_0 30.8 (38.9); 8 sequences of 2048.  128: the
+//           form for many rows 46.5, four passes of this one 60.8.  48 and 64 rows in two
+//           passes would be 3 % (Q8_0 11 %) faster there, where the second reads its keys
+//           from the caches, and read them twice from memory in a larger batch
+//   splits  few workgroups: enough splits that there are 256, of at least 128 tokens (513
+//           tokens: 12.1 us; of 256 tokens 14.4); many: up to 4096 workgroups of at least 512 tokens
+//           for the balance, at most 32 splits of a row (64 sequences of 1 to 8192: 232 us,
+//           2048 workgroups 237, 512 without splits 279; 131072 tokens in 32 splits 101, 64
+//           104, 128 111)
+//   many rows: 512 workgroups, two a CU (512 tokens over 8192: 140 us; 256 180, 1024 167)
 struct Plan {
     int mode;  // 0, 1, 2: attn_few_kernel; 3: the form for many rows
     int tiles, splits;

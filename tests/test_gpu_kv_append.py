@@ -142,6 +142,10 @@ CASES = [
     dict(dtype=8, Hq=1, Hk=1, D=96, page=32, lens=[33], new=33, rot=0, fused=False),
     dict(dtype=1, Hq=5, Hk=5, D=128, page=64, lens=[200, 129], new=65, with_q=False, fused=False),
     dict(dtype=1, Hq=16, Hk=4, D=192, page=32, lens=[5] * 70, new=5, norm=True, rot=48),
+    # from 2048 tokens on: tiles of 64 places
+    dict(dtype=1, Hq=1, Hk=2, D=96, page=16, lens=[1500, 1024], new=1024, starts=[3, 1010, 2034], rows=2040),
+    dict(dtype=8, Hq=1, Hk=1, D=192, page=64, lens=[777, 2050], new=1100, starts=[0, 500, 1600]),
+    dict(dtype=8, Hq=1, Hk=1, D=64, page=32, lens=[5, 1031, 90], new=1031, starts=[0, 5, 1036, 1099]),
     dict(dtype=8, Hq=7, Hk=1, D=128, page=64, lens=[64] * 130, new=2, starts=list(range(0, 131)), rows=140),
 ]
 
