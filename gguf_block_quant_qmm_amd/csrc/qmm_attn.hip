@@ -124,8 +124,11 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : MODE == 0 ? 3 : 2) 
     const Pages page_of(a, w.s);
     int k0 = w.k0 + kChunk * wave;
     Regs<D, Q8> x;
-    Where at{}, next{};
-    if (k0 < w.k1) at = where(page_of, k0);
+    Where at{}, next{}, after{};
+    if (k0 < w.k1) {
+        at = where(page_of, k0);
+        if constexpr (!STACK) next = where(page_of, k0 + kChunk * kWaves);
+    }
 
     // the queries' two parts (one tile: in registers, every wavefront its own; more rows:
     // in LDS, made by a wavefront a tile), and what each of the lane's columns sees
@@ -214,7 +217,12 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : MODE == 0 ? 3 : 2) 
 
     for (; k0 < w.k1; k0 += kChunk * kWaves) {
         const int kn = k0 + kChunk * kWaves;
-        if (kn < w.k1) next = where(page_of, kn);
+        // The next chunk's pages.  With more than one tile's work in a chunk they are asked for a chunk
+        // ahead, below, before the values: loads return in order, and the next keys' addresses would
+        // wait for those values (8 x 7 tokens on Q8_0: 39.4 to 36.7 us; one token over 131072: 101 here, 113 so)
+        if constexpr (STACK) {
+            if (kn < w.k1) next = where(page_of, kn);
+        }
         // scores: s[c][4 t + i] is token k0 + 8 g + 4 t + i of column c
         float s[NC][8];
         {
@@ -273,7 +281,10 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : MODE == 0 ? 3 : 2) 
                     for (int j = 0; j < 8; j++) s[c][j] = capped(s[c][j], a.softcap);
             }
         }
-        if (kn < w.k1) load_keys<D, Q8>(a, next, w.h, kn, rec, x);
+        if (kn < w.k1) {
+            load_keys<D, Q8>(a, next, w.h, kn, rec, x);
+            if constexpr (!STACK) after = where(page_of, kn + kChunk * kWaves);
+        }
 
         const bool plain = k0 >= w.lo_all && k0 + kChunk <= w.hi_all && __ballot(at.v < 0) == 0;  // uniform
         if (!plain) {
@@ -445,6 +456,7 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : MODE == 0 ? 3 : 2) 
             }
         }
         at = next;
+        if constexpr (!STACK) next = after;
         if (kn < w.k1) load_values<D, Q8>(a, at, w.h, kn, rec, x);
     }
 
