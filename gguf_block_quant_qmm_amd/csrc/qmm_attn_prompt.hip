@@ -11,8 +11,11 @@
 //                      16 scores are two runs of 8 neighbouring tokens
 // f32 class: queries and probabilities in two f16 parts, two steps for one.
 // Q8_0: codes times (both parts of) the queries, one block's product scaled by
-// the token's key scale in f32; values as hi + lo, both f16 and exact together
-// (a code times a scale has 18 bits), three steps for one.
+// the token's key scale in f32; values times 2^7 as hi + lo, both f16 and exact together (a code
+// times a scale has 18 bits and is 2^-24 at least), three steps for one: hi takes both parts of the
+// probabilities, lo (2^-11 of the value or less, and 0 where the value is below 2^-20) their first.  Times
+// 2^7, because the matrix cores align a product as if a factor below 2^-14 were as large as that.
+// Values under scales from 4 on would pass f16 so: they go through products of their own.
 //
 // Bound by the matrix cores: the products of a wavefront and tile take 2048 cycles of a SIMD at D =
 // 128, its softmax about 1100 of the vector ALU; two wavefronts a SIMD, and two halves of a
@@ -58,14 +61,24 @@ template <int D, bool Q8> struct Tile {  // in LDS
     _Float16 v[Q8 ? 2 : 1][D][VP];
     _Float16 ks[Q8 ? D / 32 : 1][CH];
     int odd[4];  // per wavefront
-    // the queries' second parts, a wavefront's own, where the registers cannot hold them and
-    // this does (16 query heads of 256, 512 tokens over 4096: 131 us, 160 with 133 registers spilled)
-    static constexpr bool QL = !Q8 && D == 256;
-    half8 ql[QL ? 4 : 1][QL ? D / 16 : 1][QL ? 64 : 1];
+    int large;   // the last tile with values under large scales
+    // the queries' second parts of the first QL steps, a wavefront's own, where the registers cannot
+    // hold them and this does (16 query heads of 256, 512 tokens over 4096: f16 131 us, 160 with 133
+    // registers spilled; Q8_0 217, with 8 steps 8 % more, with none 40 %)
+    static constexpr int QL = D != 256 ? 0 : Q8 ? 12 : 16;
+    half8 ql[QL ? 4 : 1][QL ? QL : 1][QL ? 64 : 1];
 };
 
 // Token t of a tile <-> row of the first product: bits 2 and 3 exchanged.
 __device__ __forceinline__ int swap23(int t) { return (t & ~12) | ((t & 4) << 1) | ((t & 8) >> 1); }
+
+constexpr uint32_t kLargeScale = 0x4400, kInfScale = 0x7C00;  // f16 bits: 4, from where 2^7 of a value may pass 65504
+
+// A value scale whose codes go through large_values.
+__device__ __forceinline__ bool is_large(_Float16 scale) {
+    const uint32_t u = __builtin_bit_cast(unsigned short, scale) & 0x7FFFu;
+    return u >= kLargeScale && u < kInfScale;
+}
 
 // A token's distance from the tile's first, cut to what the tile can tell apart.
 __device__ __forceinline__ int within(int x) { return x < 0 ? 0 : x > CH ? CH : x; }
@@ -88,8 +101,8 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
     attn_sees(a, w.nw, t, lo, hi);
     if (!on) lo = hi = 0;
 
-    constexpr bool QL = Tile<D, Q8>::QL;
-    half8 qh[NK], ql[QL ? 1 : NK];
+    constexpr int QL = Tile<D, Q8>::QL;
+    half8 qh[NK], ql[QL < NK ? NK - QL : 1];
     float mul;
     {
         const float *q = a.Q + (int64_t)(w.nw.first + t) * a.q_stride + (int64_t)hq * D + 8 * hh;
@@ -122,8 +135,8 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                 qh[b][i] = p;
                 rest[i] = (_Float16)(v - (float)p);
             }
-            if constexpr (QL) T.ql[wave][b][lane] = rest;
-            else ql[b] = rest;
+            if (b < QL) T.ql[wave][b][lane] = rest;
+            else ql[b - QL] = rest;
         }
     }
     floatx16 o[ND];
@@ -189,19 +202,41 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         if constexpr (Q8) {
             if (tid < 16 * NS) *reinterpret_cast<u32x2_t *>(&T.ks[tid >> 4][4 * (tid & 15)]) = st.ks;
         }
-        bool odd = false;
+        bool odd = false, large = false, some_large = false;
+        if constexpr (Q8) {
+            typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+            ushort2_t most{0, 0};
+#pragma unroll
+            for (int b = 0; b < Stage<D, Q8>::NB; b++) {
+                const u32x4_t v = __builtin_bit_cast(u32x4_t, st.vs[b]);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t u = v[j] & 0x7FFF7FFFu;
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2_t, u));
+                }
+            }
+            some_large = __ballot(most.x >= kLargeScale || most.y >= kLargeScale) != 0;  // rare
+        }
 #pragma unroll
         for (int i = 0; i < NS; i++) {
             const int d = d0 + 8 * i;
             half8 x, y;
             if constexpr (Q8) {
-                // v = 2^7 x + y exactly: 2^7 x is v to 11 bits or to 2^-17, y the rest
-                const half8 cd = codes8(st.v[i]);
+                // 2^7 v = x + y exactly: v is a multiple of its scale's last bit, 2^18 of them at most
+                const half8 cd = codes8(st.v[i]), sc = st.vs[st.at(i)] * (_Float16)128.f;
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    const float v = (float)cd[j] * (float)st.vs[st.at(i)][j];
-                    x[j] = (_Float16)(v * 0.0078125f);
-                    y[j] = (_Float16)fmaf((float)x[j], -128.f, v);
+                    const float v = (float)cd[j] * (float)sc[j];
+                    x[j] = (_Float16)v;
+                    y[j] = (_Float16)fmaf((float)x[j], m1, v);
+                }
+                if (some_large) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        if (!is_large(st.vs[st.at(i)][j])) continue;
+                        large = true;
+                        x[j] = y[j] = (_Float16)0.f;
+                    }
                 }
             } else {
                 x = __builtin_bit_cast(half8, st.v[i]);
@@ -226,8 +261,10 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         }
         if (!plain && lane == 0) T.odd[wave] = 0;
         if (odd) T.odd[wave] = 1;
+        if (large) T.large = k0;
     };
 
+    if (Q8 && tid == 0) T.large = -1;
     if (w.k0 < w.k1) load(w.k0);
     for (int k0 = w.k0; k0 < w.k1; k0 += CH) {
         const bool plain = k0 >= w.lo_all && k0 + CH <= w.hi_all && good == 15;  // uniform
@@ -237,6 +274,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         __syncthreads();
         if (k0 + CH < w.k1) load(k0 + CH);
         if (!wave_on) continue;
+        const int large_tile = T.large;
         // Two halves of 32 tokens: while the matrix cores have one half's scores or outputs, the
         // vector ALU has the other's softmax.  The products have priority, so that another
         // wavefront's softmax fills what they leave of the issue.
@@ -251,7 +289,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
 #pragma unroll
             for (int i = 0; i < AHEAD; i++) {
                 kf[i] = read(i);
-                if constexpr (QL) qr[i] = T.ql[wave][i][lane];
+                if (i < QL) qr[i] = T.ql[wave][i][lane];
             }
 #pragma unroll
             for (int i = 0; i < 16; i++) s[i] = 0.f;
@@ -261,11 +299,9 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
             for (int i = 0; i < NK; i++) {
                 if (i + AHEAD < NK) {
                     kf[(i + AHEAD) % (AHEAD + 1)] = read(i + AHEAD);
-                    if constexpr (QL) qr[(i + AHEAD) % (AHEAD + 1)] = T.ql[wave][i + AHEAD][lane];
+                    if (i + AHEAD < QL) qr[(i + AHEAD) % (AHEAD + 1)] = T.ql[wave][i + AHEAD][lane];
                 }
-                half8 qlo;
-                if constexpr (QL) qlo = qr[i % (AHEAD + 1)];
-                else qlo = ql[i];
+                const half8 qlo = i < QL ? qr[i % (AHEAD + 1)] : ql[i < QL ? 0 : i - QL];
                 if constexpr (Q8) {
                     if ((i & 1) == 0) {  // the first half of a block
 #pragma unroll
@@ -342,7 +378,6 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                 vf[i] = read(0, i);
                 if constexpr (Q8) vl[i] = read(1, i);
             }
-            half8 pd;
 #pragma unroll
             for (int i = 0; i < NK; i++) {
                 const int f = i / ND, d = i % ND;
@@ -350,14 +385,46 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                     vf[(i + AHEAD) % (AHEAD + 1)] = read(0, i + AHEAD);
                     if constexpr (Q8) vl[(i + AHEAD) % (AHEAD + 1)] = read(1, i + AHEAD);
                 }
-                if constexpr (Q8) {
-                    if (d == 0) pd = ph[f] * (_Float16)0.0078125f;
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[i % (AHEAD + 1)], pd, o[d], 0, 0, 0);
-                }
+                if constexpr (Q8) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[i % (AHEAD + 1)], ph[f], o[d], 0, 0, 0);
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[i % (AHEAD + 1)], pl[f], o[d], 0, 0, 0);
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[i % (AHEAD + 1)], ph[f], o[d], 0, 0, 0);
                 under(i);
                 __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        // The values under large scales, from memory: 2^-7 of one is hi + lo exactly.  Apart from the other
+        // products, so that a row that does not see such a token keeps its bits.
+        auto large_values = [&](int u, const half8 (&ph)[2], const half8 (&pl)[2]) {
+#pragma unroll 1
+            for (int f = 0; f < 2; f++) {
+                const half8 pa = f ? ph[1] : ph[0], pb = f ? pl[1] : pl[0];
+                const int k = k0 + 32 * u + 16 * f + 8 * hh, pk = page_of(k), slot = k & (page - 1);
+                const uint8_t *p = a.kv.v + ((int64_t)(pk < 0 ? 0 : pk) * a.kv.heads + w.h) * rec;  // masked
+#pragma unroll
+                for (int d = 0; d < ND; d++) {
+                    // addresses made here each time, not kept in registers through the main loop
+                    int dim = 32 * d + col;
+                    asm volatile("" : "+v"(dim));
+                    const half8 cd = codes8(*reinterpret_cast<const u32x2_t *>(p + dim * page + slot));
+                    const half8 sc = *reinterpret_cast<const half8 *>(p + page * D + 2 * ((dim >> 5) * page + slot));
+                    half8 x, y;
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float v = is_large(sc[j]) ? (float)cd[j] * (float)sc[j] * 0x1p-7f : 0.f;
+                        x[j] = (_Float16)v;
+                        y[j] = (_Float16)fmaf((float)x[j], m1, v);
+                        __builtin_amdgcn_sched_barrier(0);  // one at a time: no registers for a rare case
+                    }
+                    // 2^-14 of an output is exact (but for one below 2^-112)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) o[d][i] *= 0x1p-14f;
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y, pa, o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pb, o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pa, o[d], 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) o[d][i] *= 0x1p14f;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         };
         auto nothing = [](int) {};
@@ -386,6 +453,22 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         outputs(0, p0h, p0l, [&](int i) { softmax(i, s1, p1h, p1l); });
         outputs(1, p1h, p1l, nothing);
         __builtin_amdgcn_s_setprio(0);
+        if constexpr (Q8) {
+            // rare: the probabilities once more, under the reference of the tile's end (kept until
+            // here they would take 16 registers from the main loop)
+            if (__builtin_amdgcn_readfirstlane(large_tile) == k0) {
+                const float sum = l;
+#pragma unroll 1
+                for (int u = 0; u < 2; u++) {
+                    scores(u, s1, nothing);
+                    largest(u, s1);
+#pragma unroll
+                    for (int i = 0; i < NK; i++) softmax(i, s1, p1h, p1l);
+                    large_values(u, p1h, p1l);
+                }
+                l = sum;
+            }
+        }
         if (!plain && (T.odd[0] | T.odd[1] | T.odd[2] | T.odd[3])) {  // rare: infinities or NaN that only some rows see
             for (int j = 0; j < CH; j++) {
                 const int k = k0 + j;
@@ -419,7 +502,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
     if (!on) return;
     const int64_t rh = (int64_t)(w.nw.first + t) * a.Hq + hq;
     const bool none = base == -INFINITY;
-    float f = Q8 ? 128.f : 1.f;
+    float f = Q8 ? 0x1p-7f : 1.f;
     float *to = a.out + rh * D;
     if (a.splits > 1) {
         const int64_t at = rh * a.splits + w.split;
