@@ -31,6 +31,8 @@
 // next values after the second product.  The four wavefronts of a workgroup take
 // every fourth chunk and join through LDS; workgroups that share a row write their
 // sums and maxima to `work`, joined by a second launch.
+#include <float.h>
+
 #include <type_traits>
 
 #include "qmm_attn.hpp"
@@ -274,11 +276,9 @@ __global__ void __launch_bounds__(64 * kWaves, D > 128 ? 1 : MODE == 0 ? 3 : 2) 
                             v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
                         s[c][4 * t + i] = v * mul[c];
                     }
-            if (a.softcap > 0.f) {  // uniform
+            if (a.cap > 0.f) {  // uniform
 #pragma unroll
-                for (int c = 0; c < NC; c++)
-#pragma unroll
-                    for (int j = 0; j < 8; j++) s[c][j] = capped(s[c][j], a.softcap);
+                for (int c = 0; c < NC; c++) cap_scores<8>(a, s[c]);
             }
         }
         if (kn < w.k1) {
@@ -660,6 +660,9 @@ hipError_t launch_d(AttnArgs a, int dtype, const Plan &p, hipStream_t st) {
     return hipSuccess;
 }
 
+// A positive value as f32, cut to the largest.
+float f32_of(double v) { return v < FLT_MAX ? (float)v : FLT_MAX; }
+
 }  // namespace
 
 int64_t attention_work_bytes(const qmm_kv_cache &cache, const qmm_kv_batch &batch, int64_t q_heads) {
@@ -679,7 +682,13 @@ hipError_t launch_attention(const qmm_kv_cache &cache, const qmm_kv_batch &batch
     a.q_stride = q_stride;
     a.window = window;
     a.scale = (float)scale;
-    a.softcap = (float)softcap;
+    if (softcap > 0.0) {
+        const double cap = softcap * 1.44269504088896340736;
+        a.cap = f32_of(cap);
+        a.cap_inv = f32_of(1.0 / cap);
+        a.cap_from = f32_of(0.5 * cap);
+        a.cap_rate = f32_of(2.0 / softcap);  // e^(2t/c) = 2^(t rate)
+    }
     a.Hq = (int)q_heads;
     a.G = (int)(q_heads / cache.heads);
     a.splits = p.splits;

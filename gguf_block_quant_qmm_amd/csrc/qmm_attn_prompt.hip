@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         // Two halves of 32 tokens: while the matrix cores have one half's scores or outputs, the
         // vector ALU has the other's softmax.  The products have priority, so that another
         // wavefront's softmax fills what they leave of the issue.
-        const float mm = a.softcap > 0.f ? 1.f : mul;
+        const float mm = a.cap > 0.f ? 1.f : mul;
         const int from = within(lo - k0) - 8 * hh, end = within(hi - k0) - 8 * hh;
         // One step is two products (three: Q8_0's outputs), the read for the step after the next and
         // the part of a softmax that fits under them, in this order (the scheduler gathers the
@@ -327,9 +327,10 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         // softcap and mask; true if the reference has to move to `mx`
         float mx;
         auto largest = [&](int u, floatx16 &s) {
-            if (a.softcap > 0.f) {  // uniform
+            if (a.cap > 0.f) {  // uniform
 #pragma unroll
-                for (int i = 0; i < 16; i++) s[i] = capped(s[i] * mul, a.softcap);
+                for (int i = 0; i < 16; i++) s[i] *= mul;
+                cap_scores<16>(a, s);
             }
             if (!plain) {
                 // register i of half hh is token 16 (i / 8) + 8 hh + i % 8 of its 32

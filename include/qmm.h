@@ -584,7 +584,7 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
  * Queries and probabilities are split in two f16 parts under a power of two and
  * multiplied on the matrix cores, f32 accumulation, statistics in f32: f32 class.
  * With S_j = |scale| sum_d |q_d key_jd|, the error of a score is at most
- *     e_j = 2^-17 S_j + 2^-36 |scale| max_d |q_d| sum_d |key_jd| + 2^-21 softcap
+ *     e_j = 2^-17 S_j + 2^-36 |scale| max_d |q_d| sum_d |key_jd|      (a softcap: + 2^-21 |x_j|)
  * and with e its largest value over the n visible tokens,
  *     |out - exact| <= (2 e + 2^-17 + n 2^-26) sum_j p_j (|value_j| + |exact|) + n 2^-32 max_j |value_j|
  * (the last over all dims of the visible tokens).  These count every rounding at its worst;
