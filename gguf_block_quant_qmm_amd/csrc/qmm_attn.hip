@@ -31,10 +31,6 @@
 // next values after the second product.  The four wavefronts of a workgroup take
 // every fourth chunk and join through LDS; workgroups that share a row write their
 // sums and maxima to `work`, joined by a second launch.
-#include <float.h>
-
-#include <type_traits>
-
 #include "qmm_attn.hpp"
 
 namespace qmm {
@@ -681,10 +677,11 @@ hipError_t launch_attention(const qmm_kv_cache &cache, const qmm_kv_batch &batch
     a.stat = (float2 *)((char *)work + batch.rows * q_heads * p.splits * 4 * (int64_t)cache.dim);
     a.q_stride = q_stride;
     a.window = window;
-    a.scale = (float)scale;
+    constexpr double log2e = 1.44269504088896340736;
+    a.mul = (float)frexp(scale * log2e, &a.mul_exp);
     if (softcap > 0.0) {
-        const double cap = softcap * 1.44269504088896340736;
-        a.cap = f32_of(cap);
+        const double cap = softcap * log2e;
+        a.cap = fmaxf(f32_of(cap), FLT_TRUE_MIN);  // one that rounds to 0 is still a cap
         a.cap_inv = f32_of(1.0 / cap);
         a.cap_from = f32_of(0.5 * cap);
         a.cap_rate = f32_of(2.0 / softcap);  // e^(2t/c) = 2^(t rate)

@@ -3,6 +3,8 @@
 // rows' f16 parts.  Included only by the HIP sources of attention.
 #pragma once
 
+#include <float.h>
+
 #include "qmm_internal.hpp"
 #include "qmm_kv.hpp"
 
@@ -14,7 +16,8 @@ struct AttnArgs {
     float *part;   // [rows][Hq][splits][D]: sum of p * value under the split's maximum
     float2 *stat;  // [rows][Hq][splits]: (maximum, sum of p); -inf: the split saw nothing
     int64_t q_stride, window, block0;
-    float scale;
+    float mul;    // mul * 2^mul_exp: scale in base 2
+    int mul_exp;
     float cap, cap_inv, cap_from, cap_rate;  // of cap_scores; cap 0: none
     int Hq, G, splits, tiles;
     bool causal;
@@ -123,10 +126,10 @@ __device__ __forceinline__ int row_exponent(float amax) {
     return e < 126 ? e : 126;
 }
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
-// A raw product times this is the score in base 2.
-__device__ __forceinline__ float attn_mul(const AttnArgs &a, int e) { return ldexpf(a.scale * kLog2e, -e); }
+// A raw product (queries times 2^e) times this is the score in base 2.  Finite: a product of 0 has a score of 0.
+__device__ __forceinline__ float attn_mul(const AttnArgs &a, int e) {
+    return fminf(fmaxf(ldexpf(a.mul, a.mul_exp - e), -FLT_MAX), FLT_MAX);
+}
 
 // Scores t in base 2 under a softcap (c in base 2): c tanh(t / c).  Below c / 2: t (1 + P(t^2 / c^2)), which keeps the
 // bits of a score far below the cap; else c (1 - 2 / (e^(2t/c) + 1)).  Within 2^-21 of the capped score either

@@ -580,7 +580,7 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
  * causal, j <= i, and, with a window w > 0, j > i - w.  A row that sees nothing
  * gets zeros, whatever the cache holds; what a row does not see does not reach
  * it, infinities and NaN neither.  An infinity that it does see (query, key or
- * value) may come out as NaN, and an infinite key as NaN where its score would be -infinity.
+ * value) or a score beyond f32 may come out as NaN, and an infinite key as NaN where its score would be -infinity.
  * Queries and probabilities are split in two f16 parts under a power of two and
  * multiplied on the matrix cores, f32 accumulation, statistics in f32: f32 class.
  * With S_j = |scale| sum_d |q_d key_jd|, the error of a score is at most
@@ -594,7 +594,7 @@ int qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const fl
  *   q_heads a multiple of cache->heads, at most 2^16; rows * q_heads at most 2^40,
  *           max_new * q_heads / heads and seqs * heads at most 2^31 - 1: else
  *           QMM_ERR_SHAPE
- *   scale   finite; softcap finite, >= 0; window >= 0, and 0 unless causal: else
+ *   scale   finite, as f32 too; softcap the same, >= 0; window >= 0, and 0 unless causal: else
  *           QMM_ERR_VALUE
  *   out     device f32 [rows][q_heads * dim], 16-B aligned; rows of sequences
  *           overwritten, padding left as it is; overlaps nothing
