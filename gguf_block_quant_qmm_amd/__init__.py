@@ -527,7 +527,8 @@ def _on(dev, t, need: int, what: str, dtype) -> int:
 def _rows(dev, t, rows: int, width: int, stride: int, what: str, dtype) -> int:
     """Address of f32 rows of `width` values that lie `stride` values apart (0:
     side by side).  The tensor may be a view into wider rows (columns of a fused
-    projection); what the rows reach must lie inside its storage."""
+    projection, [rows][heads][dim] too), or flat; what the rows reach must lie inside
+    its storage."""
     if not stride or t is None or type(t) is int:
         return _on(dev, t, rows * width, what, dtype)
     if t.get_device() != dev:
@@ -536,7 +537,12 @@ def _rows(dev, t, rows: int, width: int, stride: int, what: str, dtype) -> int:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.dim() == 2 and t.stride() == (stride, 1) and t.shape[0] >= rows and t.shape[1] >= width:
         return t.data_ptr()
-    if t.dim() and (t.stride(-1) != 1 or (t.dim() > 1 and t.shape[0] > 1 and t.stride(0) != stride)):
+    if t.dim() > 1 and t.shape[0] > 0:
+        if t.shape[0] > 1 and t.stride(0) != stride or not t[0].is_contiguous():
+            raise ValueError(f"{what} must have rows {stride} values apart, each contiguous")
+        if (t.shape[0] > 1 or rows == 1) and (t.shape[0] < rows or t[0].numel() < width):
+            raise ValueError(f"{what} holds {t.shape[0]} rows of {t[0].numel()} values, needs {rows} of {width}")
+    elif t.dim() and t.stride(-1) != 1:
         raise ValueError(f"{what} must have rows {stride} values apart")
     if rows > 0 and width > 0:
         held = t.untyped_storage().nbytes() // 4 - t.storage_offset()
