@@ -37,7 +37,7 @@ struct TurnArgs {
     double mscale, eps;
     int Hq, Hk, D, rot, hpb, bpt;  // heads a workgroup, workgroups a token
     bool half;
-    int64_t row0, N;               // qmm_rope: rows; qmm_kv_append: kv.rows
+    int64_t row0;                  // of a launch
     int64_t turn_blocks, v0, v_tiles;
     KvArgs kv;
 };
@@ -349,7 +349,6 @@ hipError_t launch_rope(const float *X, int64_t x_stride, int64_t N, int64_t H, i
     a.D = (int)D;
     a.rot = (int)rot;
     a.half = half;
-    a.N = N;
     const int uph = (int)(D / 8);
     a.hpb = 256 / uph < H ? 256 / uph : (int)H;
     a.bpt = (int)((H + a.hpb - 1) / a.hpb);
@@ -386,7 +385,6 @@ hipError_t launch_kv_append(const qmm_kv_cache &cache, const qmm_kv_batch &batch
     a.D = cache.dim;
     a.rot = freqs ? (int)rot : 0;
     a.half = half;
-    a.N = batch.rows;
     a.kv = kv_args(cache, batch);
     a.hpb = 256 / (a.D / 8);
     a.bpt = (a.Hq + a.Hk + a.hpb - 1) / a.hpb;
