@@ -682,7 +682,7 @@ hipError_t launch_attention(const qmm_kv_cache &cache, const qmm_kv_batch &batch
     if (softcap > 0.0) {
         const double cap = softcap * log2e;
         a.cap = fmaxf(f32_of(cap), FLT_TRUE_MIN);  // one that rounds to 0 is still a cap
-        a.cap_inv = f32_of(1.0 / cap);
+        a.cap_inv = f32_of(0.60196578275345014 / cap);  // the unit that makes P's leading coefficient 1
         a.cap_from = f32_of(0.5 * cap);
         a.cap_rate = f32_of(2.0 / softcap);  // e^(2t/c) = 2^(t rate)
     }

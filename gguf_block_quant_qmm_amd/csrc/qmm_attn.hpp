@@ -134,17 +134,17 @@ __device__ __forceinline__ float attn_mul(const AttnArgs &a, int e) {
 // Scores t in base 2 under a softcap (c in base 2): c tanh(t / c).  Below c / 2: t (1 + P(t^2 / c^2)), which keeps the
 // bits of a score far below the cap; else c (1 - 2 / (e^(2t/c) + 1)).  Within 2^-21 of the capped score either
 // way, where the second alone would be 2^-22 of the cap and faster in prompts (512 tokens over 4096, 32/8 heads
-// of 128 f16: 100 us, 92 so, 83 without a cap; of 64: 73, 63, 53).  P is fitted to tanh(x) / x - 1 for the least largest
-// error of tanh, 2^-26.  Both for every score: a branch that leaves the
-// exponentials out costs registers that the kernels lack (it spills on Q8_0, calls without a cap too).
+// of 128 f16: 98 us, 90 so, 81 without a cap; of 64: 73, 62, 52).  P is fitted to tanh(x) / x - 1 for the least
+// largest error of tanh, 2^-26, and in the unit of x that leaves its leading coefficient 1: the constants are
+// then literals and hold no registers through the main loop.  Both forms for every score: a branch that leaves
+// the exponentials out costs registers that the kernels lack (it spills on Q8_0, calls without a cap too).
 template <int N, typename S>
 __device__ __forceinline__ void cap_scores(const AttnArgs &a, S &s) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const float t = s[i], x = t * a.cap_inv, z = x * x;
-        const float p = fmaf(fmaf(fmaf(0.017241476f, z, -0.053045485f), z, 0.13325879f), z, -0.33333144f);
-        const float near = t * fmaf(p, z, 1.f);
-        const float far = fmaf(-2.f * a.cap, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(t * a.cap_rate) + 1.f), a.cap);
+        const float near = t * fmaf(fmaf(fmaf(z + -1.11485296f, z, 1.01486586f), z, -0.919883146f), z, 1.f);
+        const float far = a.cap * fmaf(-2.f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(t * a.cap_rate) + 1.f), 1.f);
         s[i] = fabsf(t) < a.cap_from ? near : far;
         if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // four at a time
     }

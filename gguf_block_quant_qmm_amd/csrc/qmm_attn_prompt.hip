@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         }
         bool odd = false, large = false, some_large = false;
         if constexpr (Q8) {
+            // (a negative scale, which no quantizer makes, is looked at below too)
             typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
             ushort2_t most{0, 0};
 #pragma unroll
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                 const u32x4_t v = __builtin_bit_cast(u32x4_t, st.vs[b]);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const uint32_t u = v[j] & 0x7FFF7FFFu;
+                    const uint32_t u = v[j];
                     most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2_t, u));
                 }
             }
