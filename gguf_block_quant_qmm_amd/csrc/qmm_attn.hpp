@@ -84,7 +84,8 @@ __device__ __forceinline__ bool attn_share(const AttnArgs &a, int least, AttnSha
     return true;
 }
 
-// A sequence's row of the page table; token i's page (0 <= i <= 2^30 + 64), or -1.
+// A sequence's row of the page table; token i's page, or -1.  i >= 0; the kernels ask up to 300 tokens past a
+// sequence's end, so past the 2^30 of the longest table too.
 struct Pages {
     const int32_t *row;
     int shift, columns, pages;

@@ -17,12 +17,13 @@
 // 2^7, because the matrix cores align a product as if a factor below 2^-14 were as large as that.
 // Values under scales from 4 on would pass f16 so: they go through products of their own.
 //
-// Bound by the matrix cores: the products of a wavefront and tile take 2048 cycles of a SIMD at D =
-// 128, its softmax about 1100 of the vector ALU; two wavefronts a SIMD, and two halves of a
-// tile in each, let one's softmax run under the other's products.  512 tokens over 8192,
-// 32/8 heads of 128 f16: 134 us (matrix cores busy 54 %, 1000 TFLOP/s of f16 steps where the library's
-// plain product reaches 1160 to 1180) and 10 for the join.  At D = 64 the vector ALU bounds
-// it (half the products for the same softmax): 512 over 4096 54 us.  Keys and
+// Bound by the matrix cores and by what a tile waits for: the products of a wavefront and tile take 2048
+// cycles of a SIMD at D = 128, its softmax about 1100 of the vector ALU; two wavefronts a SIMD, and two
+// halves of a tile in each, let one's softmax run under the other's products.  512 tokens over 8192,
+// 32/8 heads of 128 f16: 133 us, 150 as the clock comes down (1000 to 880 TFLOP/s of f16 steps where the
+// library's plain product reaches 1160 to 1180; matrix cores busy in 48 % of the cycles, vector ALU in 35) and 11
+// for the join.  At D = 64, half the products for the same softmax, neither is half busy (ragged Q8_0
+// prompts: 22 and 43 %, a wavefront waits in 38 % of its cycles); 512 over 4096 51 us, Q8_0 65.  Keys and
 // values go through registers to LDS (rows padded by 16 bytes: eight neighbouring rows
 // then start in eight different groups of four banks), the next tile's loads under
 // way during the products.

@@ -11,8 +11,8 @@
 //
 // Bound by memory (one read, one write; about 6 f64 operations a pair): 4096 tokens of 40
 // heads of 128 take 33 us, 5.1 TB/s, the rate of a large copy; one token of 32 heads 3.0 us, of
-// which a launch is about 2.  Appending 4096 tokens of 32/8 heads to f16 pages takes 42 us
-// (185 MB, 4.4 TB/s).  A workgroup takes one token and up to 256 units of 8 values (for halves, 4
+// which a launch is about 2.  Appending 4096 tokens of 32/8 heads to f16 pages takes 42 to 44 us
+// (185 MB, 4.2 to 4.4 TB/s), to Q8_0 pages 3 more (177 MB).  A workgroup takes one token and up to 256 units of 8 values (for halves, 4
 // neighbours of either half), one per thread, so that the loads are under way
 // while a wavefront works out the angles.
 //
