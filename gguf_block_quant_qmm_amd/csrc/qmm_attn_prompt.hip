@@ -65,7 +65,7 @@ template <int D, bool Q8> struct Tile {  // in LDS
     int large;   // the last tile with values under large scales
     // the queries' second parts of the first QL steps, a wavefront's own, where the registers cannot
     // hold them and this does (16 query heads of 256, 512 tokens over 4096: f16 131 us, 160 with 133
-    // registers spilled; Q8_0 217, with 8 steps 8 % more, with none 40 %)
+    // registers spilled; Q8_0 222, with 8 steps 8 % more, with none 40 %)
     static constexpr int QL = D != 256 ? 0 : Q8 ? 12 : 16;
     half8 ql[QL ? 4 : 1][QL ? QL : 1][QL ? 64 : 1];
 };
@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
         if constexpr (Q8) {
             if (tid < 16 * NS) *reinterpret_cast<u32x2_t *>(&T.ks[tid >> 4][4 * (tid & 15)]) = st.ks;
         }
-        bool odd = false, large = false, some_large = false;
+        bool odd = false, large = false;
         if constexpr (Q8) {
-            // (a negative scale, which no quantizer makes, is looked at below too)
+            // values under large scales are taken out here, like those that no row sees, and come from large_values
+            // (a negative scale, which no quantizer makes, is looked at too)
             typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
             ushort2_t most{0, 0};
 #pragma unroll
@@ -217,7 +218,16 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                     most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2_t, u));
                 }
             }
-            some_large = __ballot(most.x >= kLargeScale || most.y >= kLargeScale) != 0;  // rare
+            if (__ballot(most.x >= kLargeScale || most.y >= kLargeScale)) {  // rare
+#pragma unroll
+                for (int b = 0; b < Stage<D, Q8>::NB; b++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        if (!is_large(st.vs[b][j])) continue;
+                        large = true;
+                        st.vs[b][j] = (_Float16)0.f;
+                    }
+            }
         }
 #pragma unroll
         for (int i = 0; i < NS; i++) {
@@ -231,14 +241,6 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) attn_prompt_kernel(cons
                     const float v = (float)cd[j] * (float)sc[j];
                     x[j] = (_Float16)v;
                     y[j] = (_Float16)fmaf((float)x[j], m1, v);
-                }
-                if (some_large) {
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        if (!is_large(st.vs[st.at(i)][j])) continue;
-                        large = true;
-                        x[j] = y[j] = (_Float16)0.f;
-                    }
                 }
             } else {
                 x = __builtin_bit_cast(half8, st.v[i]);
