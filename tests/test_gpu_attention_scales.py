@@ -88,15 +88,15 @@ SIZES = [(4, 1, 64, 16, 300, 1), (4, 1, 96, 16, 90, 4), (8, 2, 128, 32, 260, 7),
          (1, 1, 256, 64, 700, 130)]
 
 
-def rescale(c, values, spread, r):
-    """Gives the tokens of sequence 0 the scales of `spread`, in order."""
-    n, blocks, page = c.lens[0], c.D // 32, c.page
+def rescale(c, values, spread, r, s=0):
+    """Gives the tokens of sequence s the scales of `spread`, in order."""
+    n, blocks, page = c.lens[s], c.D // 32, c.page
     size = page * c.D
     rec = (c.v_pool if values else c.k_pool).reshape(c.pages, c.Hk, -1)
     for h in range(c.Hk):
         sc = spread(r, n, blocks).astype(np.float16)
         for i in range(n):
-            rec[c.table[0, i // page], h, size:].view(np.float16).reshape(blocks, page)[:, i % page] = sc[i]
+            rec[c.table[s, i // page], h, size:].view(np.float16).reshape(blocks, page)[:, i % page] = sc[i]
 
 
 @pytest.mark.parametrize("spread", SPREADS, ids=lambda f: f.__name__)
@@ -153,3 +153,30 @@ def test_a_scale_that_a_row_does_not_see_does_not_reach_it(new, scale):
         outs.append(c.out.clone())
     assert torch.equal(outs[0][:new // 2], outs[1][:new // 2])
     assert not torch.equal(outs[0][new // 2:], outs[1][new // 2:])
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_scales_masks_and_pages(seed):
+    """Scales of every size beside windows, ragged rows, other sequences and pages that are none."""
+    r = np.random.default_rng([78, seed])
+    D, Hk, G = int(r.choice([64, 96, 128, 192, 256])), int(r.choice([1, 2])), int(r.choice([1, 2, 4]))
+    page, seqs, new = int(r.choice([16, 32, 64])), int(r.integers(1, 4)), int(r.choice([1, 7, 40, 90]))
+    lens = [int(r.integers(1, 400)) for _ in range(seqs)]
+    kw = {}
+    if r.random() < 0.5:
+        n = [int(r.integers(0, new + 1)) for _ in range(seqs)]
+        kw["starts"] = [int(v) for v in np.cumsum([r.integers(0, 3)] + n)]
+        kw["rows"] = max(1, kw["starts"][-1] + int(r.integers(0, 4)))
+    if r.random() < 0.3:
+        kw["causal"] = False
+    elif r.random() < 0.5:
+        kw["window"] = int(r.choice([3, 31, 100]))
+    c = Case(8, G * Hk, Hk, D, page, lens, new, seed=seed, cap=float(r.choice([0.0, 0.0, 15.0])), **kw)
+    for s in range(seqs):
+        rescale(c, True, SPREADS[int(r.integers(len(SPREADS)))], r, s)
+    if r.random() < 0.4:
+        hit = r.random(c.table.shape) < 0.25
+        c.table[hit] = r.choice([-1, c.pages, 2 ** 31 - 1, -2 ** 31], hit.sum()).astype(np.int32)
+    c.buffers().call()
+    torch.cuda.synchronize()
+    c.check()
