@@ -7,9 +7,9 @@
 //
 // Bound by memory: every key and value is read once for all G query heads of its
 // head and all new tokens (32/8 heads of 128, f16: one token over 131072 96 us and 5 for the join,
-// 5.6 TB/s; 64 sequences of 1 to 8192 226 + 7 us, 5.4 TB/s); few rounds of a
+// 5.6 TB/s; 64 sequences of 1 to 8192 225 + 7 us, 5.4 TB/s); few rounds of a
 // wavefront by latency (28 rows on a Q8_0 cache, 8 x 7 tokens to 4096: 33 + 5 us, a wavefront waits in 43 %
-// of its cycles, vector ALU busy in 27; 513 tokens: 8.9 + 3.9).  The matrix cores do the products, because a row of f32
+// of its cycles, vector ALU busy in 27; 513 tokens: 8.6 + 4.0).  The matrix cores do the products, because a row of f32
 // FMAs would cost as many instructions per query head as there are bytes:
 //   scores^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens' keys (a lane's 8
 //                      values are 16 bytes of its token's key), B = 16 columns of

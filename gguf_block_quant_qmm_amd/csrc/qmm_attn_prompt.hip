@@ -20,10 +20,10 @@
 // Bound by the matrix cores and by what a tile waits for: the products of a wavefront and tile take 2048
 // cycles of a SIMD at D = 128, its softmax about 1100 of the vector ALU; two wavefronts a SIMD, and two
 // halves of a tile in each, let one's softmax run under the other's products.  512 tokens over 8192,
-// 32/8 heads of 128 f16: 133 us, 150 as the clock comes down (1000 to 880 TFLOP/s of f16 steps where the
-// library's plain product reaches 1160 to 1180; matrix cores busy in 48 % of the cycles, vector ALU in 35) and 11
+// 32/8 heads of 128 f16: 133 us, 147 (median of 60) as the clock comes down (1000 and 905 TFLOP/s of f16 steps, where the
+// library's plain product reaches 1160 to 1180; matrix cores busy in 48 % of the cycles, vector ALU in 36) and 11
 // for the join.  At D = 64, half the products for the same softmax, neither is half busy (ragged Q8_0
-// prompts: 22 and 43 %, a wavefront waits in 38 % of its cycles); 512 over 4096 51 us, Q8_0 65.  Keys and
+// prompts: 23 and 43 %, a wavefront waits in 38 % of its cycles); 512 over 4096 51 us, Q8_0 65.  Keys and
 // values go through registers to LDS (rows padded by 16 bytes: eight neighbouring rows
 // then start in eight different groups of four banks), the next tile's loads under
 // way during the products.
