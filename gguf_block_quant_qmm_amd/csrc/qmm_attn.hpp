@@ -144,7 +144,7 @@ __device__ __forceinline__ void cap_scores(const AttnArgs &a, S &s) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const float t = s[i], x = t * a.cap_inv, z = x * x;
-        const float near = t * fmaf(fmaf(fmaf(z + -1.11485296f, z, 1.01486586f), z, -0.919883146f), z, 1.f);
+        const float near = t * fmaf(fmaf(fmaf(z - 1.11485296f, z, 1.01486586f), z, -0.919883146f), z, 1.f);
         const float far = a.cap * fmaf(-2.f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(t * a.cap_rate) + 1.f), 1.f);
         s[i] = fabsf(t) < a.cap_from ? near : far;
         if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // four at a time
